@@ -24,7 +24,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libentropack.so")
 
-BF16, FP16, FP8_E4M3, F32, INT8 = 1, 2, 3, 4, 5
+BF16, FP16, FP8_E4M3, F32, INT8, MXFP4, NVFP4 = 1, 2, 3, 4, 5, 6, 7
 _TORCH_TO_EP = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: FP8_E4M3,
                 torch.float32: F32, torch.int8: INT8}
 _EP_TO_TORCH = {v: k for k, v in _TORCH_TO_EP.items()}
@@ -44,6 +44,21 @@ class EpTensor(ctypes.Structure):
 class EpOptions(ctypes.Structure):
     _fields_ = [("steps_per_tile", _I), ("num_threads", _I), ("scale", _D), ("rd_refine", _I),
                 ("host_encoder", _I), ("prob_bits", _I)]
+
+
+class EpFP4Tensor(ctypes.Structure):
+    _fields_ = [("data", _P), ("scales", _P), ("tensor_scale", _P), ("device", _I), ("format", _I),
+                ("rows", _I64), ("cols", _I64)]
+
+
+class EpCache(ctypes.Structure):
+    _fields_ = [("data", _P), ("scales", _P), ("device", _I), ("format", _I), ("n_pages", _I64),
+                ("page_size", _I), ("heads", _I), ("head_dim", _I)]
+
+
+class EpHeads(ctypes.Structure):
+    _fields_ = [("data", _P), ("device", _I), ("dtype", _I), ("tokens", _I64), ("heads", _I), ("head_dim", _I),
+                ("token_stride", _I64), ("head_stride", _I64)]
 
 
 class EpBlobInfo(ctypes.Structure):
@@ -68,6 +83,14 @@ SIGNATURES = {
     "ep_decompress_noalloc": (_I, [_P, _P, _SZ, ctypes.POINTER(EpTensor), _P, _I]),
     "ep_decode_wait_probe": (_I, [_P, ctypes.c_uint32, _P]),
     "ep_decompress_fp8_rowscaled": (_I, [_P, ctypes.POINTER(EpTensor), _P, _P]),
+    "ep_fp4_sizes": (_I, [_I, _I64, _I64, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)]),
+    "ep_fp4_quantize": (_I, [ctypes.POINTER(EpTensor), ctypes.POINTER(EpFP4Tensor), _D, _P]),
+    "ep_fp4_dequantize": (_I, [ctypes.POINTER(EpFP4Tensor), ctypes.POINTER(EpTensor), _P]),
+    "ep_decompress_fp4": (_I, [_P, ctypes.POINTER(EpFP4Tensor), _D, ctypes.POINTER(EpTensor), _P]),
+    "ep_fp4_matmul": (_I, [ctypes.POINTER(EpFP4Tensor), ctypes.POINTER(EpFP4Tensor), _P, ctypes.POINTER(EpTensor), _P]),
+    "ep_cache_write": (_I, [ctypes.POINTER(EpCache), ctypes.POINTER(EpHeads), _I, _P, _P]),
+    "ep_cache_read": (_I, [ctypes.POINTER(EpCache), ctypes.POINTER(EpHeads), _I, _P, _I64, _I64, _I, _P, _P]),
+    "ep_op_status": (_I, [_P]),
     "ep_blob_free": (None, [_P]),
     "ep_last_error": (ctypes.c_char_p, []),
 }
@@ -300,6 +323,11 @@ def decode_fields(compressed: CompressedTensor, stream=None) -> torch.Tensor:
     return out
 
 
+from .operators import (FP4Tensor, KVCache, cache_read, cache_write, decompress_fp4, fp4_dequantize,  # noqa: E402
+                        fp4_matmul, fp4_quantize, op_status)
+
 __all__ = ["LatticeRANSConfig", "CompressedTensor", "compress", "decompress", "decompress_group",
            "decompress_fp8_rowscaled", "decode_status",
-           "decode_fields", "EPError", "lib", "BF16", "FP16", "FP8_E4M3", "F32", "INT8"]
+           "decode_fields", "EPError", "lib", "BF16", "FP16", "FP8_E4M3", "F32", "INT8", "MXFP4", "NVFP4",
+           "FP4Tensor", "fp4_quantize", "fp4_dequantize", "fp4_matmul", "decompress_fp4", "KVCache", "cache_write",
+           "cache_read", "op_status"]

@@ -19,11 +19,12 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libentropack.so")
-PLAIN = ["api.cpp", "encoder.cpp", "decode.cu", "encode_gpu.cu"]
+PLAIN = ["api.cpp", "encoder.cpp", "decode.cu", "encode_gpu.cu", "ops.cpp", "fp4.cu", "fp4_matmul.cu", "cache.cu"]
 # The decode kernels: decode_unit.cu once per output container (OutKind 0..6) and table layout.
 UNIT_OUTS = range(7)
 UNIT_LAYS = (10, 11, 12, 13, 14, 15)
-HEADERS = ["format.h", "blob.h", "tables.h", "decode_launch.h", "decode_device.cuh"]
+HEADERS = ["format.h", "blob.h", "tables.h", "decode_launch.h", "decode_device.cuh", "ops.h", "microscale.cuh",
+           "tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -1,0 +1,432 @@
+// cache.cu -- the quantised key/value cache: ep_cache_write and ep_cache_read.  The formats are
+// defined in entropack.h; the 4-bit block arithmetic is in microscale.cuh.
+#include <algorithm>
+#include <string>
+
+#include "blob.h"
+#include "microscale.cuh"
+#include "ops.h"
+
+namespace ep {
+namespace {
+
+using namespace ms;
+
+constexpr int kThreads = 256;
+constexpr int kMaxHeadDim = 1024;
+constexpr int kLaunchTokens = 4096;  // tokens of one write launch
+constexpr int kMaxWriteTokens = 8;   // tokens of one block of a write
+constexpr int kReadTokens = 16;      // tokens of one block of a read
+constexpr int kSharedSeqs = 1024;    // sequence starts that a read searches in shared memory
+
+struct CacheView {
+    uint8_t* data;
+    uint8_t* scales;
+    int64_t row_bytes;
+    int64_t scale_bytes;  // of one row: 4, or one a block
+    void* heads;          // source or output rows
+    int64_t token_stride, head_stride;
+    int head_dim;
+    int lanes;            // lanes of one row: a power of two, 8 elements each (4 x 8 above 256)
+    bool vec;             // rows are 16-byte aligned and whole chunks of 8
+};
+
+struct WriteArgs {
+    CacheView c[2];
+    const int64_t* slots;
+    int64_t n_slots;      // n_pages * page_size
+    int64_t tokens;       // of this launch
+    int heads;
+    int per_block;        // tokens of one block
+};
+
+struct ReadArgs {
+    CacheView c[2];
+    const int32_t* page_table;
+    int64_t table_stride, pages_per_seq, n_pages, tokens;
+    const int32_t* cu_seqlens;
+    int n_seqs, page_size, heads;
+};
+
+// ---- writing -----------------------------------------------------------------------------------
+
+// The smallest power of two s with amax <= 448 s (448 = 1.75 * 2^8), at least 2^-100.
+__device__ __forceinline__ int e4m3_row_exponent(float amax) {
+    const int m = __float_as_int(amax) & 0x7fffff;
+    return max(log2_floor(amax) - 8 + (m > 0x600000 ? 1 : 0), -100);
+}
+
+// The integer nearest v / s, ties to even: a candidate from the reciprocal, at most one off, and the
+// exact remainder v - n s (it is a multiple of the smaller of the two units in the last place and
+// not much above s, so the fma does not round it) to settle the border.
+__device__ __forceinline__ int nearest_quotient(float v, float s, float inv) {
+    const float n = rintf(v * inv);
+    const float r = __fmaf_rn(-n, s, v), h = 0.5f * s;
+    int i = int(n);
+    if (r > h || (r == h && (i & 1))) ++i;
+    if (r < -h || (r == -h && (i & 1))) --i;
+    return i;
+}
+
+// The payload (and by its first lane the scale) of one row, of which this lane holds chunks of 8
+// elements `lane`, `lane + lanes`, ...; v[k] are zeros past the row's end.
+template <int DT, int FMT, int NC>
+__device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int lane, float (&v)[NC][8], bool live) {
+    uint8_t* data = c.data + row * c.row_bytes;
+    uint8_t* scales = c.scales + row * c.scale_bytes;
+    if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
+        float amax = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) amax = max_abs(amax, abs_max8(v[k]));
+        amax = lanes_max(amax, c.lanes);
+        const bool fine = is_finite(amax);
+        float s, inv;
+        if constexpr (FMT == EP_FP8_E4M3) {
+            const int e = e4m3_row_exponent(amax);
+            s = pow2f(e);
+            inv = pow2f(-e);
+        } else {
+            s = amax >= 0x1p-100f ? __fdiv_rn(amax, 127.0f) : 0.0f;
+            inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+        }
+        if (!fine) s = __int_as_float(0x7fc00000);
+        if (!live) return;
+        if (lane == 0) *reinterpret_cast<float*>(scales) = s;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            const int at = 8 * (lane + k * c.lanes);
+            if (at >= c.head_dim) break;
+            uint32_t w[2] = {0, 0};
+            if (fine && inv > 0.0f) {
+                if constexpr (FMT == EP_FP8_E4M3) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint16_t two;
+                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(v[k][2 * j + 1] * inv), "f"(v[k][2 * j] * inv));
+                        w[j / 2] |= uint32_t(two) << (16 * (j % 2));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        w[j / 4] |= uint32_t(nearest_quotient(v[k][j], s, inv) & 0xff) << (8 * (j % 4));
+                }
+            }
+            if (c.head_dim % 8 == 0) {  // 8-byte aligned: the pool is, and so is every row
+                *reinterpret_cast<uint2*>(data + at) = make_uint2(w[0], w[1]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (at + j < c.head_dim) data[at + j] = uint8_t(w[j / 4] >> (8 * (j % 4)));
+            }
+        }
+    } else {
+        constexpr bool NV = FMT == EP_NVFP4;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            const int chunk = lane + k * c.lanes, at = 8 * chunk;
+            const float amax = lanes_max(abs_max8(v[k]), NV ? 2 : 4);
+            const Block b = block_scale<NV>(amax, 1.0f, 1.0f);
+            const uint32_t codes = quantize8<DT, NV>(v[k], b);
+            if (!live || at / 2 >= c.row_bytes) continue;
+            *reinterpret_cast<uint32_t*>(data + at / 2) = codes;
+            if (chunk % (NV ? 2 : 4) == 0 && at < c.head_dim) scales[chunk / (NV ? 2 : 4)] = uint8_t(b.byte);
+        }
+    }
+}
+
+// A block takes a few tokens, all heads.  First it looks through the later tokens of the launch for
+// its own slots: a token whose slot is named again later is dropped, so that payload and scale of a
+// slot always come from one token (launches of one call follow each other, the later wins).
+template <int DT, int FMT, int NC>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a) {
+    using T = typename Elem<DT>::T;
+    __shared__ int64_t slot[kMaxWriteTokens];
+    __shared__ int dropped[kMaxWriteTokens];
+    wait_for_stream();
+    const CacheView& c = a.c[blockIdx.y];
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
+    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
+    if (int(threadIdx.x) < n) {
+        const int64_t s = a.slots[t0 + threadIdx.x];
+        slot[threadIdx.x] = s >= 0 && s < a.n_slots ? s : -1;
+        dropped[threadIdx.x] = 0;
+    }
+    __syncthreads();
+    int64_t lo = a.n_slots, hi = -1;
+    for (int i = 0; i < n; ++i)
+        if (slot[i] >= 0) lo = min(lo, slot[i]), hi = max(hi, slot[i]);
+    if (hi >= 0)
+        for (int64_t j = t0 + 1 + threadIdx.x; j < a.tokens; j += kThreads) {
+            const int64_t s = a.slots[j];
+            if (s < lo || s > hi) continue;
+            for (int i = 0; i < n; ++i)
+                if (slot[i] == s && t0 + i < j) dropped[i] = 1;
+        }
+    __syncthreads();
+
+    const int lanes = c.lanes, lane = threadIdx.x % lanes;
+    const int step = kThreads / lanes, rows = n * a.heads;
+    // every lane of a warp stays in the loop: rows past the end are read as zeros and not written
+    for (int base = 0; base < rows; base += step) {
+        const int r = base + int(threadIdx.x) / lanes;
+        const int i = min(r / a.heads, n - 1), h = r % a.heads;
+        const bool live = r < rows && slot[i] >= 0 && !dropped[i];
+        const T* src = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride;
+        float v[NC][8];
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            const int at = 8 * (lane + k * lanes);
+            const int m = live ? max(0, min(8, c.head_dim - at)) : 0;
+            if (c.vec && m == 8) raw_to_float8<DT>(load_raw8<DT>(src + at), v[k]);
+            else load_some<DT>(src + at, m, v[k]);
+        }
+        write_row<DT, FMT, NC>(c, slot[i] * a.heads + h, lane, v, live);
+    }
+}
+
+// ---- reading -----------------------------------------------------------------------------------
+
+template <int DT, int FMT>
+__device__ __forceinline__ void read_chunk(const CacheView& c, int64_t row, int chunk, typename Elem<DT>::T* dst) {
+    const int at = 8 * chunk;
+    if (at >= c.head_dim) return;
+    float v[8];
+    if (row < 0) {  // no such page
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    } else {
+        const uint8_t* data = c.data + row * c.row_bytes;
+        const uint8_t* scales = c.scales + row * c.scale_bytes;
+        if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
+            uint32_t w[2] = {0, 0};
+            if (c.head_dim % 8 == 0) {
+                const uint2 u = *reinterpret_cast<const uint2*>(data + at);
+                w[0] = u.x;
+                w[1] = u.y;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (at + j < c.head_dim) w[j / 4] |= uint32_t(data[at + j]) << (8 * (j % 4));
+            }
+            const float s = *reinterpret_cast<const float*>(scales);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t two = (w[j / 2] >> (16 * (j % 2))) & 0xffffu;
+                const float2 f = FMT == EP_FP8_E4M3
+                                     ? e4m3x2_value(two)
+                                     : make_float2(float(int8_t(two & 0xff)), float(int8_t(two >> 8)));
+                v[2 * j] = f.x * s;
+                v[2 * j + 1] = f.y * s;
+            }
+        } else {
+            constexpr bool NV = FMT == EP_NVFP4;
+            e2m1_values8(*reinterpret_cast<const uint32_t*>(data + at / 2), v);
+            const float s = scale_value<NV>(scales[chunk / (NV ? 2 : 4)]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= s;
+        }
+    }
+    if (c.vec) store8<DT>(dst + at, v);
+    else store_some<DT>(dst + at, min(8, c.head_dim - at), v);
+}
+
+// The last sequence that starts at or before token t.
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seqs, int64_t t) {
+    int lo = 0, hi = n_seqs;  // cu[lo] <= t < cu[hi], if t is in any sequence
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (int64_t(cu[mid]) <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// A block takes 16 tokens of the output, all heads: finds their slots, then its threads take chunks
+// of 8 elements.
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) {
+    using T = typename Elem<DT>::T;
+    __shared__ int32_t starts[kSharedSeqs + 1];
+    __shared__ int64_t slot[kReadTokens];  // -1: zeros, -2: past the sequences
+    wait_for_stream();
+    const CacheView& c = a.c[blockIdx.y];
+    const int64_t t0 = int64_t(blockIdx.x) * kReadTokens;
+    const int n = int(min(int64_t(kReadTokens), a.tokens - t0));
+    const bool shared = a.n_seqs <= kSharedSeqs;
+    if (shared)
+        for (int i = threadIdx.x; i <= a.n_seqs; i += kThreads) starts[i] = a.cu_seqlens[i];
+    __syncthreads();
+    if (int(threadIdx.x) < n) {
+        const int32_t* cu = shared ? starts : a.cu_seqlens;
+        const int64_t t = t0 + threadIdx.x;
+        int64_t s = -2;
+        const int seq = sequence_of(cu, a.n_seqs, t);
+        const int64_t pos = t - cu[seq];
+        if (pos >= 0 && t < cu[seq + 1]) {
+            s = -1;
+            const int64_t p = pos / a.page_size;
+            if (p < a.pages_per_seq) {
+                const int64_t page = a.page_table[seq * a.table_stride + p];
+                if (page >= 0 && page < a.n_pages) s = page * a.page_size + pos % a.page_size;
+            }
+        }
+        slot[threadIdx.x] = s;
+    }
+    __syncthreads();
+    const int chunks = (c.head_dim + 7) / 8, per_token = a.heads * chunks;
+    for (int i = threadIdx.x; i < n * per_token; i += kThreads) {
+        const int t = i / per_token, h = i % per_token / chunks, chunk = i % chunks;
+        if (slot[t] == -2) continue;
+        T* dst = static_cast<T*>(c.heads) + (t0 + t) * c.token_stride + h * c.head_stride;
+        read_chunk<DT, FMT>(c, slot[t] < 0 ? -1 : slot[t] * a.heads + h, chunk, dst);
+    }
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+template <int DT, int FMT>
+cudaError_t launch_write(const WriteArgs& w, int n, bool wide, cudaStream_t st) {
+    const dim3 grid(unsigned(op::div_up(w.tokens, w.per_block)), unsigned(n));
+    return op::launch(wide ? cache_write_kernel<DT, FMT, 4> : cache_write_kernel<DT, FMT, 1>, grid, dim3(kThreads), 0, st, w);
+}
+template <int DT>
+cudaError_t write_as(int fmt, const WriteArgs& w, int n, bool wide, cudaStream_t st) {
+    switch (fmt) {
+        case EP_FP8_E4M3: return launch_write<DT, EP_FP8_E4M3>(w, n, wide, st);
+        case EP_INT8: return launch_write<DT, EP_INT8>(w, n, wide, st);
+        case EP_MXFP4: return launch_write<DT, EP_MXFP4>(w, n, wide, st);
+        default: return launch_write<DT, EP_NVFP4>(w, n, wide, st);
+    }
+}
+template <int DT, int FMT>
+cudaError_t launch_read(const ReadArgs& r, int n, cudaStream_t st) {
+    const dim3 grid(unsigned(op::div_up(r.tokens, kReadTokens)), unsigned(n));
+    return op::launch(cache_read_kernel<DT, FMT>, grid, dim3(kThreads), 0, st, r);
+}
+template <int DT>
+cudaError_t read_as(int fmt, const ReadArgs& r, int n, cudaStream_t st) {
+    switch (fmt) {
+        case EP_FP8_E4M3: return launch_read<DT, EP_FP8_E4M3>(r, n, st);
+        case EP_INT8: return launch_read<DT, EP_INT8>(r, n, st);
+        case EP_MXFP4: return launch_read<DT, EP_MXFP4>(r, n, st);
+        default: return launch_read<DT, EP_NVFP4>(r, n, st);
+    }
+}
+
+// Checks caches and the tensors that go with them, and fills the views the kernels read.
+int make_views(const ep_cache* caches, const ep_heads* h, int n, const char* who, CacheView* out) {
+    const std::string w(who);
+    for (int i = 0; i < n; ++i) {
+        const ep_cache& c = caches[i];
+        const ep_heads& x = h[i];
+        const bool fp4 = op::is_fp4(c.format);
+        if (!fp4 && c.format != EP_FP8_E4M3 && c.format != EP_INT8) return set_error(EP_ERR_DTYPE, w + ": unsupported cache format");
+        const int es = op::elem_bytes(x.dtype);
+        if (es == 0) return set_error(EP_ERR_DTYPE, w + ": heads must be EP_BF16, EP_FP16 or EP_F32");
+        if (c.n_pages < 0 || c.page_size < 1 || c.heads < 1 || c.head_dim < 1 || c.head_dim > kMaxHeadDim || c.heads > 65536 ||
+            c.n_pages > (int64_t(1) << 40) / c.page_size)
+            return set_error(EP_ERR_SHAPE, w + ": cache geometry out of range");
+        if (x.tokens < 0 || x.tokens > 0x7fffffff || x.heads != c.heads || x.head_dim != c.head_dim)
+            return set_error(EP_ERR_SHAPE, w + ": heads do not match the cache");
+        if (c.format != caches[0].format || c.n_pages != caches[0].n_pages || c.page_size != caches[0].page_size ||
+            c.heads != caches[0].heads || x.tokens != h[0].tokens)
+            return set_error(EP_ERR_SHAPE, w + ": the caches of one call differ in geometry");
+        if (x.dtype != h[0].dtype) return set_error(EP_ERR_DTYPE, w + ": the heads of one call differ in type");
+        if (x.token_stride < 0 || x.head_stride < 0) return set_error(EP_ERR_ARG, w + ": negative stride");
+        if (c.n_pages > 0 && (!c.data || !c.scales || !op::aligned(c.data, 16) || !op::aligned(c.scales, fp4 ? 1 : 4)))
+            return set_error(EP_ERR_ARG, w + ": cache data or scales are NULL or misaligned");
+        if (x.tokens > 0 && (!x.data || !op::aligned(x.data, size_t(es))))
+            return set_error(EP_ERR_ARG, w + ": heads are NULL or misaligned");
+        CacheView& v = out[i];
+        v.data = static_cast<uint8_t*>(c.data);
+        v.scales = static_cast<uint8_t*>(c.scales);
+        v.row_bytes = fp4 ? op::fp4_row_bytes(c.head_dim) : c.head_dim;
+        v.scale_bytes = fp4 ? op::fp4_blocks(c.format, c.head_dim) : 4;
+        v.heads = x.data;
+        v.token_stride = x.token_stride;
+        v.head_stride = x.head_stride;
+        v.head_dim = c.head_dim;
+        v.lanes = 4;  // a 4-bit block is 2 or 4 lanes
+        while (v.lanes < 32 && 8 * v.lanes < c.head_dim) v.lanes *= 2;
+        v.vec = c.head_dim % 8 == 0 && op::aligned(x.data, 16) && (x.token_stride * es) % 16 == 0 && (x.head_stride * es) % 16 == 0;
+    }
+    return EP_OK;
+}
+
+// The current device, which must be the caches' and heads' own.
+int device_of(const ep_cache* caches, const ep_heads* h, int n, const char* who, int& sms) {
+    int dev = 0;
+    const int rc = op::current_device(dev, sms);
+    if (rc != EP_OK) return rc;
+    for (int i = 0; i < n; ++i)
+        if (caches[i].device != dev || h[i].device != dev)
+            return set_error(EP_ERR_ARG, std::string(who) + ": a tensor is not on the current device");
+    return EP_OK;
+}
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n, const int64_t* slots, void* stream) {
+    clear_error();
+    if (!caches || !src || n < 1 || n > 2) return set_error(EP_ERR_ARG, "ep_cache_write: NULL argument, or not one or two caches");
+    int sms = 0;
+    WriteArgs w = {};
+    int rc = make_views(caches, src, n, "ep_cache_write", w.c);
+    if (rc != EP_OK) return rc;
+    const int64_t tokens = src[0].tokens;
+    if (tokens > 0 && (!slots || !op::aligned(slots, 8))) return set_error(EP_ERR_ARG, "ep_cache_write: slots are NULL or misaligned");
+    rc = device_of(caches, src, n, "ep_cache_write", sms);
+    if (rc != EP_OK || tokens == 0 || caches[0].n_pages == 0) return rc;
+    const bool wide = src[0].head_dim > 256 || (n == 2 && src[1].head_dim > 256);
+    const int es = op::elem_bytes(src[0].dtype);
+    w.n_slots = caches[0].n_pages * caches[0].page_size;
+    w.heads = caches[0].heads;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    for (int64_t t0 = 0; t0 < tokens; t0 += kLaunchTokens) {
+        WriteArgs part = w;
+        part.slots = slots + t0;
+        part.tokens = std::min<int64_t>(kLaunchTokens, tokens - t0);
+        for (int i = 0; i < n; ++i)
+            part.c[i].heads = static_cast<uint8_t*>(w.c[i].heads) + t0 * w.c[i].token_stride * es;
+        // few tokens are spread over as many blocks as there are SMs
+        part.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxWriteTokens, part.tokens * n / (2 * sms))));
+        const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, n, wide, st)
+                              : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, n, wide, st)
+                                                        : write_as<EP_F32>(caches[0].format, part, n, wide, st);
+        if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_cache_write: ") + cudaGetErrorString(e));
+    }
+    return EP_OK;
+}
+
+extern "C" int ep_cache_read(const ep_cache* caches, const ep_heads* out, int n, const int32_t* page_table, int64_t table_stride,
+                             int64_t pages_per_seq, int n_seqs, const int32_t* cu_seqlens, void* stream) {
+    clear_error();
+    if (!caches || !out || n < 1 || n > 2) return set_error(EP_ERR_ARG, "ep_cache_read: NULL argument, or not one or two caches");
+    int sms = 0;
+    ReadArgs r = {};
+    int rc = make_views(caches, out, n, "ep_cache_read", r.c);
+    if (rc != EP_OK) return rc;
+    if (n_seqs < 0 || pages_per_seq < 0 || table_stride < pages_per_seq)
+        return set_error(EP_ERR_ARG, "ep_cache_read: bad sequence count or page table");
+    if (!cu_seqlens || !op::aligned(cu_seqlens, 4) || (n_seqs > 0 && pages_per_seq > 0 && (!page_table || !op::aligned(page_table, 4))))
+        return set_error(EP_ERR_ARG, "ep_cache_read: page_table or cu_seqlens is NULL or misaligned");
+    rc = device_of(caches, out, n, "ep_cache_read", sms);
+    if (rc != EP_OK || n_seqs == 0 || out[0].tokens == 0) return rc;
+    r.page_table = page_table;
+    r.table_stride = table_stride;
+    r.pages_per_seq = pages_per_seq;
+    r.n_pages = caches[0].n_pages;
+    r.tokens = out[0].tokens;
+    r.cu_seqlens = cu_seqlens;
+    r.n_seqs = n_seqs;
+    r.page_size = caches[0].page_size;
+    r.heads = caches[0].heads;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = out[0].dtype == EP_BF16   ? read_as<EP_BF16>(caches[0].format, r, n, st)
+                          : out[0].dtype == EP_FP16 ? read_as<EP_FP16>(caches[0].format, r, n, st)
+                                                    : read_as<EP_F32>(caches[0].format, r, n, st);
+    if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_cache_read: ") + cudaGetErrorString(e));
+    return EP_OK;
+}

@@ -1,0 +1,396 @@
+// fp4.cu -- the microscaled 4-bit container: ep_fp4_sizes, ep_fp4_quantize, ep_fp4_dequantize and
+// ep_decompress_fp4.  The formats are defined in entropack.h, their arithmetic in microscale.cuh.
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "blob.h"
+#include "microscale.cuh"
+#include "ops.h"
+
+namespace ep {
+namespace {
+
+using namespace ms;
+
+constexpr int kTileRows = 128;   // a block handles 128 rows x 128 columns: whole 512-byte scale
+constexpr int kTileCols = 128;   // tiles (two for blocks of 16), written at once
+constexpr int kThreads = 256;
+constexpr int kPassRows = kThreads / (kTileCols / 8);  // 16 threads a row, 8 elements each
+constexpr int kPasses = kTileRows / kPassRows;
+constexpr int kMaxPartials = EP_FP4_SCALE_FLOATS - 1;
+
+struct QuantArgs {
+    const void* x;
+    int64_t stride, rows, cols;
+    uint8_t* data;
+    uint8_t* scales;
+    float* tensor_scale;
+    int64_t row_bytes;
+    int col_tiles;    // blocks side by side
+    int scale_tiles;  // 512-byte scale tiles side by side
+    float fixed;      // > 0: the tensor scale
+    int partials;     // > 0: its maxima are in tensor_scale[1 ..]; 0 and no fixed scale: each block
+                      // looks at all of x
+    bool vec;         // rows are 16-byte aligned
+};
+
+// Eight elements from column c of a row, zeros past the last column.
+template <int DT>
+__device__ __forceinline__ void load_row8(const typename Elem<DT>::T* row, int64_t c, int64_t cols, bool vec, float* v) {
+    if (vec && c + 8 <= cols) raw_to_float8<DT>(load_raw8<DT>(row + c), v);
+    else load_some<DT>(row + c, int(max(int64_t(0), min(int64_t(8), cols - c))), v);
+}
+
+// The largest finite |v| of eight.
+__device__ __forceinline__ float finite_max8(const float* v) {
+    float m = abs_max8(v);
+    if (!is_finite(m)) {
+        m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (is_finite(fabsf(v[j]))) m = fmaxf(m, fabsf(v[j]));
+    }
+    return m;
+}
+
+// The largest of a block's threads, in all of them.
+__device__ __forceinline__ float block_max(float m, float* smem) {
+    m = lanes_max(m, 32);
+    if (threadIdx.x % 32 == 0) smem[threadIdx.x / 32] = m;
+    __syncthreads();
+    m = smem[threadIdx.x % (kThreads / 32)];
+    m = lanes_max(m, kThreads / 32);
+    return m;
+}
+
+// Chunks of eight elements `first`, `first + step`, ... of x, row by row.
+template <int DT>
+__device__ __forceinline__ float max_of_chunks(const QuantArgs& a, int64_t first, int64_t step) {
+    using T = typename Elem<DT>::T;
+    const int64_t per_row = (a.cols + 7) / 8, n = a.rows * per_row;
+    const T* x = static_cast<const T*>(a.x);
+    float m = 0.0f;
+    if (a.vec && a.cols % 8 == 0) {
+        // eight loads in flight; rows without gaps need no division
+        const bool flat = a.stride == a.cols;
+        for (int64_t i = first; i < n; i += 4 * step) {
+            Raw8<DT> r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t j = min(i + k * step, n - 1);
+                r[k] = load_raw8<DT>(flat ? x + 8 * j : x + (j / per_row) * a.stride + 8 * (j % per_row));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float v[8];
+                raw_to_float8<DT>(r[k], v);
+                m = fmaxf(m, finite_max8(v));
+            }
+        }
+        return m;
+    }
+    for (int64_t i = first; i < n; i += step) {
+        float v[8];
+        const int64_t row = i / per_row;
+        load_row8<DT>(x + row * a.stride, 8 * (i - row * per_row), a.cols, a.vec, v);
+        m = fmaxf(m, finite_max8(v));
+    }
+    return m;
+}
+
+// First pass over x for a tensor scale: block i's maximum goes to tensor_scale[1 + i].
+template <int DT>
+__global__ void __launch_bounds__(kThreads) amax_kernel(const QuantArgs a) {
+    __shared__ float smem[kThreads / 32];
+    wait_for_stream();
+    const float m = block_max(
+        max_of_chunks<DT>(a, int64_t(blockIdx.x) * kThreads + threadIdx.x, int64_t(gridDim.x) * kThreads), smem);
+    if (threadIdx.x == 0) a.tensor_scale[1 + blockIdx.x] = m;
+}
+
+// One pass: a block reads its 128 x 128 elements (8 loads a thread in flight), forms the block
+// scales among 2 or 4 neighbouring threads, writes 4 bytes of codes a thread and its scale tiles.
+template <int DT, bool NV>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
+    using T = typename Elem<DT>::T;
+    __shared__ float red[kThreads / 32];
+    __shared__ __align__(16) uint8_t sc[NV ? 1024 : 512];
+    wait_for_stream();
+    const int64_t row0 = int64_t(blockIdx.x / a.col_tiles) * kTileRows;
+    const int64_t col = int64_t(blockIdx.x % a.col_tiles) * kTileCols + 8 * (threadIdx.x % 16);
+    const int sub = threadIdx.x / 16;
+    const T* x = static_cast<const T*>(a.x) + (row0 + sub) * a.stride;
+
+    float v[kPasses][8];
+    const int n = int(max(int64_t(0), min(int64_t(8), a.cols - col)));
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const bool in = row0 + sub + p * kPassRows < a.rows;
+        const T* src = x + int64_t(p) * kPassRows * a.stride + col;
+        if (a.vec && n == 8 && in) raw_to_float8<DT>(load_raw8<DT>(src), v[p]);
+        else load_some<DT>(src, in ? n : 0, v[p]);
+    }
+    float g = 1.0f;
+    if constexpr (NV) {
+        if (a.fixed > 0.0f) {
+            g = a.fixed;
+        } else {
+            float m = 0.0f;
+            if (a.partials > 0)
+                for (int i = threadIdx.x; i < a.partials; i += kThreads) m = fmaxf(m, a.tensor_scale[1 + i]);
+            else
+                m = max_of_chunks<DT>(a, threadIdx.x, kThreads);
+            g = tensor_scale_of(block_max(m, red));
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.tensor_scale[0] = g;
+    const float g_inv = 1.0f / g;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int r = sub + p * kPassRows;
+        const float amax = lanes_max(abs_max8(v[p]), NV ? 2 : 4);
+        const Block b = block_scale<NV>(amax, g, g_inv);
+        const uint32_t codes = quantize8<DT, NV>(v[p], b);
+        const bool in = row0 + r < a.rows;
+        if (in && col < 2 * a.row_bytes)
+            *reinterpret_cast<uint32_t*>(a.data + (row0 + r) * a.row_bytes + col / 2) = codes;
+        const int k = (threadIdx.x % 16) / (NV ? 2 : 4);  // the block's column in this tile
+        if (threadIdx.x % (NV ? 2 : 4) == 0)
+            sc[(k / 4) * 512 + 16 * (r % 32) + 4 * (r / 32) + k % 4] = in && col < a.cols ? b.byte : 0;
+    }
+    __syncthreads();
+    const int64_t st = int64_t(blockIdx.x % a.col_tiles) * (NV ? 2 : 1);
+    const int tiles = int(min(int64_t(NV ? 2 : 1), a.scale_tiles - st));
+    if (int(threadIdx.x) < 32 * tiles)
+        reinterpret_cast<uint4*>(a.scales + ((row0 / kTileRows) * a.scale_tiles + st) * 512)[threadIdx.x] =
+            reinterpret_cast<const uint4*>(sc)[threadIdx.x];
+}
+
+__global__ void set_scale_kernel(float* tensor_scale, float g) {
+    wait_for_stream();
+    *tensor_scale = g;
+}
+
+struct DequantArgs {
+    const uint8_t* data;
+    const uint8_t* scales;
+    const float* tensor_scale;
+    void* out;
+    int64_t stride, rows, cols, row_bytes;
+    int col_tiles, scale_tiles;
+    bool vec;
+};
+
+// The same blocks backwards: scale tiles to shared memory, 4 bytes of codes a thread, 8 elements out.
+template <int DT, bool NV>
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs a) {
+    using T = typename Elem<DT>::T;
+    __shared__ __align__(16) uint8_t sc[NV ? 1024 : 512];
+    wait_for_stream();
+    const int64_t row0 = int64_t(blockIdx.x / a.col_tiles) * kTileRows;
+    const int64_t col = int64_t(blockIdx.x % a.col_tiles) * kTileCols + 8 * (threadIdx.x % 16);
+    const int sub = threadIdx.x / 16;
+    const int64_t st = int64_t(blockIdx.x % a.col_tiles) * (NV ? 2 : 1);
+    const int tiles = int(min(int64_t(NV ? 2 : 1), a.scale_tiles - st));
+    if (int(threadIdx.x) < 32 * tiles)
+        reinterpret_cast<uint4*>(sc)[threadIdx.x] =
+            reinterpret_cast<const uint4*>(a.scales + ((row0 / kTileRows) * a.scale_tiles + st) * 512)[threadIdx.x];
+    const float g = *a.tensor_scale;
+    uint32_t codes[kPasses];
+    const bool col_in = col < a.cols;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int64_t r = row0 + sub + p * kPassRows;
+        codes[p] = col_in && r < a.rows ? *reinterpret_cast<const uint32_t*>(a.data + r * a.row_bytes + col / 2) : 0;
+    }
+    __syncthreads();
+    if (!col_in) return;
+    const int n = int(min(int64_t(8), a.cols - col));
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int r = sub + p * kPassRows;
+        if (row0 + r >= a.rows) break;
+        const int k = (threadIdx.x % 16) / (NV ? 2 : 4);
+        const float s = scale_value<NV>(sc[(k / 4) * 512 + 16 * (r % 32) + 4 * (r / 32) + k % 4]);
+        float v[8];
+        e2m1_values8(codes[p], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * s * g;
+        T* dst = static_cast<T*>(a.out) + (row0 + r) * a.stride + col;
+        if (a.vec && n == 8) store8<DT>(dst, v);
+        else store_some<DT>(dst, n, v);
+    }
+}
+
+template <int DT>
+cudaError_t launch_quantize(const QuantArgs& q, bool nv, int64_t grid, int amax_grid, cudaStream_t st) {
+    if (amax_grid > 0) {
+        cudaError_t e = op::launch(amax_kernel<DT>, dim3(unsigned(amax_grid)), dim3(kThreads), 0, st, q);
+        if (e != cudaSuccess) return e;
+    }
+    return op::launch(nv ? quantize_kernel<DT, true> : quantize_kernel<DT, false>, dim3(unsigned(grid)), dim3(kThreads), 0,
+                      st, q);
+}
+template <int DT>
+cudaError_t launch_dequantize(const DequantArgs& q, bool nv, int64_t grid, cudaStream_t st) {
+    return op::launch(nv ? dequantize_kernel<DT, true> : dequantize_kernel<DT, false>, dim3(unsigned(grid)),
+                      dim3(kThreads), 0, st, q);
+}
+
+// Tensors of at most this many bytes are searched for their largest value by every block itself
+// (from L2, one launch); larger ones in a pass of their own.  1 x 8192 bf16 with the search in each
+// of its 64 blocks: see the table of measurements beside ep_fp4_quantize below.
+constexpr int64_t kSearchBytes = 128 << 10;
+
+int check_dense(const ep_tensor* t, const char* what, const char* who) {
+    const std::string w = std::string(who) + ": " + what;
+    const int es = op::elem_bytes(t->dtype);
+    if (es == 0) return set_error(EP_ERR_DTYPE, w + " must be EP_BF16, EP_FP16 or EP_F32");
+    if (t->rows < 0 || t->cols < 0) return set_error(EP_ERR_SHAPE, w + " has a negative size");
+    if (t->rows > 0 && t->cols > 0) {
+        if (!t->data) return set_error(EP_ERR_ARG, w + " has no data");
+        if (!op::aligned(t->data, size_t(es))) return set_error(EP_ERR_ARG, w + " is not aligned to its elements");
+        if (t->row_stride < t->cols) return set_error(EP_ERR_ARG, w + ": row_stride < cols");
+    }
+    return EP_OK;
+}
+
+int check_quantize(const ep_tensor* x, const ep_fp4_tensor* out, double tensor_scale, const char* who) {
+    int rc = check_dense(x, "the matrix", who);
+    if (rc == EP_OK) rc = op::check_fp4(out, who);
+    if (rc != EP_OK) return rc;
+    if (x->rows != out->rows || x->cols != out->cols)
+        return set_error(EP_ERR_SHAPE, std::string(who) + ": the 4-bit tensor's shape differs from the matrix's");
+    int e = 0;
+    const bool ok = tensor_scale == 0.0 ||
+                    (out->format == EP_NVFP4 && tensor_scale > 0.0 && std::isfinite(tensor_scale) &&
+                     std::frexp(tensor_scale, &e) == 0.5 && e - 1 >= -100 && e - 1 <= 117);
+    if (!ok)
+        return set_error(EP_ERR_ARG, std::string(who) + (out->format == EP_NVFP4
+                                                             ? ": tensor_scale must be 0 or a power of two in [2^-100, 2^117]"
+                                                             : ": EP_MXFP4 has no tensor scale"));
+    return EP_OK;
+}
+
+// The current device, which must be the tensors' own.
+int device_of(int a, int b, const char* who, int& sms) {
+    int dev = 0;
+    const int rc = op::current_device(dev, sms);
+    if (rc == EP_OK && (a != dev || b != dev))
+        return set_error(EP_ERR_ARG, std::string(who) + ": a tensor is not on the current device");
+    return rc;
+}
+
+int quantize(const ep_tensor* x, const ep_fp4_tensor* out, double tensor_scale, cudaStream_t st, int sms, const char* who) {
+    const bool nv = out->format == EP_NVFP4;
+    cudaError_t e;
+    if (x->rows == 0 || x->cols == 0) {
+        const float g = !nv ? 1.0f : tensor_scale > 0.0 ? float(tensor_scale) : std::ldexp(1.0f, -100);
+        e = op::launch(set_scale_kernel, dim3(1), dim3(1), 0, st, out->tensor_scale, g);
+    } else {
+        QuantArgs q = {};
+        const int es = op::elem_bytes(x->dtype);
+        q.x = x->data;
+        q.stride = x->row_stride;
+        q.rows = x->rows;
+        q.cols = x->cols;
+        q.data = static_cast<uint8_t*>(out->data);
+        q.scales = static_cast<uint8_t*>(out->scales);
+        q.tensor_scale = out->tensor_scale;
+        q.row_bytes = op::fp4_row_bytes(x->cols);
+        q.col_tiles = int(op::div_up(x->cols, kTileCols));
+        q.scale_tiles = int(op::div_up(op::fp4_blocks(out->format, x->cols), 4));
+        q.fixed = float(tensor_scale);
+        q.vec = op::aligned(x->data, 16) && (x->row_stride * es) % 16 == 0;
+        const int64_t grid = op::div_up(x->rows, kTileRows) * q.col_tiles;
+        if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, std::string(who) + ": the matrix is too large");
+        int amax_grid = 0;
+        if (nv && tensor_scale == 0.0 && x->rows * x->cols * es > kSearchBytes) {
+            amax_grid = int(std::min<int64_t>({kMaxPartials, 4 * int64_t(sms), op::div_up(x->rows * x->cols, 8 * 4 * kThreads)}));
+            q.partials = amax_grid;
+        }
+        e = x->dtype == EP_BF16   ? launch_quantize<EP_BF16>(q, nv, grid, amax_grid, st)
+            : x->dtype == EP_FP16 ? launch_quantize<EP_FP16>(q, nv, grid, amax_grid, st)
+                                  : launch_quantize<EP_F32>(q, nv, grid, amax_grid, st);
+    }
+    if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string(who) + ": " + cudaGetErrorString(e));
+    return EP_OK;
+}
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_fp4_sizes(int format, int64_t rows, int64_t cols, size_t* data_bytes, size_t* scale_bytes) {
+    clear_error();
+    if (!data_bytes || !scale_bytes) return set_error(EP_ERR_ARG, "ep_fp4_sizes: NULL argument");
+    if (!op::is_fp4(format)) return set_error(EP_ERR_DTYPE, "ep_fp4_sizes: not a 4-bit format");
+    if (rows < 0 || cols < 0 || cols > op::kMaxFp4Cols || rows > op::kMaxFp4Rows)
+        return set_error(EP_ERR_SHAPE, "ep_fp4_sizes: size out of range");
+    *data_bytes = size_t(rows) * size_t(op::fp4_row_bytes(cols));
+    *scale_bytes = 512 * size_t(op::div_up(rows, 128)) * size_t(op::div_up(op::fp4_blocks(format, cols), 4));
+    return EP_OK;
+}
+
+extern "C" int ep_fp4_quantize(const ep_tensor* x, const ep_fp4_tensor* out, double tensor_scale, void* stream) {
+    clear_error();
+    if (!x || !out) return set_error(EP_ERR_ARG, "ep_fp4_quantize: NULL argument");
+    int sms = 0;
+    int rc = check_quantize(x, out, tensor_scale, "ep_fp4_quantize");
+    if (rc == EP_OK) rc = device_of(x->device, out->device, "ep_fp4_quantize", sms);
+    if (rc != EP_OK) return rc;
+    return quantize(x, out, tensor_scale, static_cast<cudaStream_t>(stream), sms, "ep_fp4_quantize");
+}
+
+extern "C" int ep_fp4_dequantize(const ep_fp4_tensor* x, const ep_tensor* out, void* stream) {
+    clear_error();
+    if (!x || !out) return set_error(EP_ERR_ARG, "ep_fp4_dequantize: NULL argument");
+    int sms = 0;
+    int rc = op::check_fp4(x, "ep_fp4_dequantize");
+    if (rc == EP_OK) rc = check_dense(out, "the output", "ep_fp4_dequantize");
+    if (rc != EP_OK) return rc;
+    if (x->rows != out->rows || x->cols != out->cols)
+        return set_error(EP_ERR_SHAPE, "ep_fp4_dequantize: the output's shape differs from the 4-bit tensor's");
+    rc = device_of(x->device, out->device, "ep_fp4_dequantize", sms);
+    if (rc != EP_OK) return rc;
+    if (x->rows == 0 || x->cols == 0) return EP_OK;
+    DequantArgs q = {};
+    q.data = static_cast<const uint8_t*>(x->data);
+    q.scales = static_cast<const uint8_t*>(x->scales);
+    q.tensor_scale = x->tensor_scale;
+    q.out = out->data;
+    q.stride = out->row_stride;
+    q.rows = x->rows;
+    q.cols = x->cols;
+    q.row_bytes = op::fp4_row_bytes(x->cols);
+    q.col_tiles = int(op::div_up(x->cols, kTileCols));
+    q.scale_tiles = int(op::div_up(op::fp4_blocks(x->format, x->cols), 4));
+    q.vec = op::aligned(out->data, 16) && (out->row_stride * op::elem_bytes(out->dtype)) % 16 == 0;
+    const int64_t grid = op::div_up(x->rows, kTileRows) * q.col_tiles;
+    if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_dequantize: the tensor is too large");
+    const bool nv = x->format == EP_NVFP4;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = out->dtype == EP_BF16   ? launch_dequantize<EP_BF16>(q, nv, grid, st)
+                          : out->dtype == EP_FP16 ? launch_dequantize<EP_FP16>(q, nv, grid, st)
+                                                  : launch_dequantize<EP_F32>(q, nv, grid, st);
+    if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_dequantize: ") + cudaGetErrorString(e));
+    return EP_OK;
+}
+
+extern "C" int ep_decompress_fp4(const ep_blob* b, const ep_fp4_tensor* out, double tensor_scale, const ep_tensor* work,
+                                 void* stream) {
+    clear_error();
+    if (!b || !out || !work) return set_error(EP_ERR_ARG, "ep_decompress_fp4: NULL argument");
+    int sms = 0;
+    int rc = check_quantize(work, out, tensor_scale, "ep_decompress_fp4");
+    if (rc != EP_OK) return rc;
+    if (work->rows != b->layout.rows || work->cols != b->layout.cols)
+        return set_error(EP_ERR_SHAPE, "ep_decompress_fp4: the work tensor's shape differs from the blob's");
+    rc = device_of(work->device, out->device, "ep_decompress_fp4", sms);
+    if (rc != EP_OK) return rc;
+    rc = ep_decompress(b, work, stream);
+    if (rc != EP_OK) return rc;
+    return quantize(work, out, tensor_scale, static_cast<cudaStream_t>(stream), sms, "ep_decompress_fp4");
+}

@@ -1,0 +1,436 @@
+// fp4_matmul.cu -- ep_fp4_matmul: out = a * transpose(b) + bias for two microscaled 4-bit matrices,
+// on the block-scaled 4-bit tensor cores.
+#include <algorithm>
+#include <atomic>
+#include <string>
+
+#include "blob.h"
+#include "microscale.cuh"
+#include "ops.h"
+#include "tcgen05.cuh"
+
+namespace ep {
+namespace {
+
+using namespace tc;
+
+constexpr int kStepK = 256;     // elements of K a pipeline stage holds: 128 bytes of a row
+constexpr int kThreads = 192;   // warp 0 copies, warp 1 issues products, warps 2 to 5 read the sums
+
+// Sticky word of products that gave up a wait, read and cleared by ep_op_status.
+__device__ uint32_t ep_op_status_word;
+
+struct MatmulArgs {
+    const uint8_t* p_scales;   // of the operand whose rows are the tensor core's 128 lanes
+    const uint8_t* q_scales;   // of the operand whose rows are its columns
+    const float* ga;
+    const float* gb;
+    const void* bias;
+    void* out;
+    int64_t stride;            // of out's rows
+    int64_t p_rows, q_rows;
+    int scale_tiles;           // 512-byte scale tiles along K
+    int steps;                 // stages along K
+    int k64;                   // products of 64 along K
+    int p_tiles;
+    int out_dtype;
+    bool vec;                  // out's rows are 16-byte aligned
+};
+
+// Tile sizes, stage layout and tensor memory columns of a variant with tiles of NT columns.
+template <int NT, bool NV>
+struct Geo {
+    static constexpr int kScaleTiles = NV ? 4 : 2;            // scale tiles of 128 rows x one stage
+    static constexpr int kQBlocks = (NT + 127) / 128;
+    static constexpr int kP = 128 * 128, kQ = NT * 128;       // bytes of the operands' stage tiles
+    static constexpr int kPS = kScaleTiles * 512, kQS = kQBlocks * kScaleTiles * 512;
+    static constexpr int kStage = kP + kQ + kPS + kQS;
+    static constexpr bool kPair = NT < 256;                   // two CTAs share an SM
+    static constexpr int kBudget = (kPair ? 113 : 226) * 1024;
+    static constexpr int kStages = (kBudget - 2048) / kStage < 8 ? (kBudget - 2048) / kStage : 8;
+    static constexpr int kSum = NT < 32 ? 32 : NT;            // accumulator columns
+    static constexpr int kScaleCols = 4 * kScaleTiles * (1 + kQBlocks);  // of one stage
+    static constexpr int kColumns = kSum + kStages * kScaleCols <= 256 ? 256 : 512;
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 256;
+    static_assert(kStages >= 3, "a pipeline of at least three stages");
+    static_assert(kSum + kStages * kScaleCols <= (kPair ? 256 : 512), "tensor memory");
+    static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
+    static_assert(kStages * kStage >= 128 * NT * 4, "partial sums fit the stages");
+};
+
+__device__ __forceinline__ float bias_at(const MatmulArgs& a, int64_t n) {
+    if (!a.bias) return 0.0f;
+    if (a.out_dtype == EP_F32) return static_cast<const float*>(a.bias)[n];
+    if (a.out_dtype == EP_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(a.bias)[n]);
+    return __half2float(static_cast<const __half*>(a.bias)[n]);
+}
+
+// `n` neighbouring elements (N at most) of row i from column j on.
+template <int N>
+__device__ __forceinline__ void store_run(const MatmulArgs& a, int64_t i, int64_t j, int n, const float* v) {
+    const int64_t at = i * a.stride + j;
+    if (a.out_dtype == EP_F32) {
+        float* o = static_cast<float*>(a.out) + at;
+        if (a.vec && n == N) {
+#pragma unroll
+            for (int k = 0; k < N; k += 4) *reinterpret_cast<float4*>(o + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                if (k < n) o[k] = v[k];
+        }
+        return;
+    }
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k)
+        w[k] = a.out_dtype == EP_BF16 ? ms::pack2<EP_BF16>(v[2 * k], v[2 * k + 1]) : ms::pack2<EP_FP16>(v[2 * k], v[2 * k + 1]);
+    uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+    if (a.vec && n == N) {
+        if constexpr (N == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+        else
+#pragma unroll
+            for (int k = 0; k < N; k += 8)
+                *reinterpret_cast<uint4*>(o + k) = make_uint4(w[k / 2], w[k / 2 + 1], w[k / 2 + 2], w[k / 2 + 3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k < n) o[k] = uint16_t(w[k / 2] >> (16 * (k % 2)));
+    }
+}
+
+// One cluster per tile of 128 rows of p x NT rows of q; its CTAs share the stages along K and then
+// the tile's columns: each adds up its share of columns over all CTAs' partial sums, in rank order.
+// SWAP: p holds b's rows (out's columns) and q a's; else p holds a's rows.
+template <int NT, bool SWAP, bool NV>
+__global__ void __launch_bounds__(kThreads) fp4_matmul_kernel(const __grid_constant__ CUtensorMap p_map,
+                                                               const __grid_constant__ CUtensorMap q_map, const MatmulArgs a) {
+    using G = Geo<NT, NV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    const uint32_t base = smem_addr(smem);
+    const uint32_t bars = base + G::kStages * G::kStage;  // full, empty of each stage; done; the TMEM address
+    auto full = [&](int s) { return bars + 8 * s; };
+    auto empty = [&](int s) { return bars + 8 * (G::kStages + s); };
+    const uint32_t done = bars + 16 * G::kStages, slot = done + 8;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    uint32_t ranks, rank = cluster_rank();
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+    const int tile = int(blockIdx.x / ranks);
+    const int p0 = (tile % a.p_tiles) * 128, q0 = (tile / a.p_tiles) * NT;
+    const int k0 = int(int64_t(a.steps) * rank / ranks), steps = int(int64_t(a.steps) * (rank + 1) / ranks) - k0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            bar_init(full(s), 1);
+            bar_init(empty(s), 1);
+        }
+        bar_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tmem_alloc(slot, G::kColumns);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+    ms::wait_for_stream();
+
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            const bool second = G::kQBlocks == 2 && q0 + 128 < a.q_rows;
+            int issued = 0;
+            for (int it = 0; it < steps && ok; ++it) {
+                const int s = it % G::kStages, k = k0 + it;
+                if (it >= G::kStages) ok = bar_wait(empty(s), (it / G::kStages - 1) & 1);
+                if (!ok) break;
+                const int tiles = min(G::kScaleTiles, a.scale_tiles - k * G::kScaleTiles);
+                const uint32_t st = base + s * G::kStage;
+                bar_expect(full(s), G::kP + G::kQ + 512 * tiles * (second ? 3 : 2));
+                tma_2d(st, &p_map, 128 * k, p0, full(s));
+                tma_2d(st + G::kP, &q_map, 128 * k, q0, full(s));
+                const int64_t at = int64_t(k) * G::kScaleTiles;
+                bulk_copy(st + G::kP + G::kQ, a.p_scales + (int64_t(p0 / 128) * a.scale_tiles + at) * 512, 512 * tiles, full(s));
+                for (int b = 0; b < (second ? 2 : 1); ++b)
+                    bulk_copy(st + G::kP + G::kQ + G::kPS * (1 + b),
+                              a.q_scales + ((int64_t(q0) / 128 + b) * a.scale_tiles + at) * 512, 512 * tiles, full(s));
+                issued = it + 1;
+            }
+            // nothing may still be on its way into this CTA's memory when it leaves
+            for (int it = max(0, issued - G::kStages); it < issued; ++it) ok &= bar_wait(full(it % G::kStages), (it / G::kStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int it = 0; it < steps; ++it) {
+                const int s = it % G::kStages;
+                ok = bar_wait(full(s), (it / G::kStages) & 1);
+                if (!ok) break;
+                fence_after();
+                const uint32_t st = base + s * G::kStage;
+                const uint32_t sp = tmem + G::kSum + s * G::kScaleCols, sq = sp + 4 * G::kScaleTiles;
+                const int products = min(4, a.k64 - 4 * (k0 + it)), tiles = NV ? products : (products + 1) / 2;
+                for (int t = 0; t < tiles; ++t) {
+                    copy_scales(sp + 4 * t, scale_desc(st + G::kP + G::kQ + 512 * t));
+#pragma unroll
+                    for (int b = 0; b < G::kQBlocks; ++b)
+                        copy_scales(sq + 4 * (t * G::kQBlocks + b), scale_desc(st + G::kP + G::kQ + G::kPS * (1 + b) + 512 * t));
+                }
+                const uint64_t da = operand_desc(st), db = operand_desc(st + G::kP);
+                for (int j = 0; j < products; ++j) {
+                    const int t = NV ? j : j / 2;
+                    mma_fp4<NV>(tmem, da + 2 * j, db + 2 * j, mma_fp4_idesc<NV>(NT, j % 2), sp + 4 * t, sq + 4 * G::kQBlocks * t,
+                                it > 0 || j > 0);
+                }
+                commit(empty(s));
+            }
+            commit(done);
+        }
+        __syncwarp();
+    }
+    // every warp: the sums are ready, and no copy or product uses the stages any more
+    ok &= bar_wait(done, 0);
+    fence_after();
+
+    const float alpha = *a.ga * *a.gb;
+    const int64_t lane0 = p0, col0 = q0;
+    if (ranks == 1 && !SWAP) {
+        if (warp >= 2) {
+            const int row = (warp % 4) * 32 + lane;
+            for (int c = 0; c < NT; c += 16) {
+                uint32_t r[16];
+                __syncwarp();
+                tmem_load16(tmem + (uint32_t(warp % 4) << 21) + c, r);
+                tmem_wait_load();
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    v[j] = __uint_as_float(r[j]) * alpha;
+                    if (a.bias && col0 + c + j < a.q_rows) v[j] += bias_at(a, col0 + c + j);
+                }
+                const int n = int(max(int64_t(0), min(int64_t(16), a.q_rows - col0 - c)));
+                if (ok && lane0 + row < a.p_rows && n > 0) store_run<16>(a, lane0 + row, col0 + c, n, v);
+            }
+        }
+        fence_before();
+        __syncthreads();
+    } else {
+        float* part = reinterpret_cast<float*>(smem);  // [column][lane]
+        if (warp >= 2) {
+            const int row = (warp % 4) * 32 + lane;
+            for (int c = 0; c < NT; c += 16) {
+                uint32_t r[16];
+                __syncwarp();
+                tmem_load16(tmem + (uint32_t(warp % 4) << 21) + c, r);
+                tmem_wait_load();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) part[(c + j) * 128 + row] = __uint_as_float(r[j]);
+            }
+        }
+        fence_before();
+        __syncwarp();
+        cluster_sync();
+        // this CTA's columns: whole groups of 8 where 8 neighbours are stored at once
+        constexpr int kGroup = SWAP ? 1 : 8;
+        const int c0 = NT / kGroup * int(rank) / int(ranks) * kGroup, c1 = NT / kGroup * (int(rank) + 1) / int(ranks) * kGroup;
+        if (SWAP) {
+            const int64_t n0 = lane0 + 4 * lane;
+            const int n = int(max(int64_t(0), min(int64_t(4), a.p_rows - n0)));
+            float bias[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bias[j] = j < n ? bias_at(a, n0 + j) : 0.0f;
+            for (int c = c0 + warp; c < c1 && col0 + c < a.q_rows; c += kThreads / 32) {
+                float v[4] = {};
+                for (uint32_t r = 0; r < ranks; ++r) {
+                    const float4 f = peer_load4(base + 4 * (c * 128 + 4 * lane), r);
+                    v[0] += f.x;
+                    v[1] += f.y;
+                    v[2] += f.z;
+                    v[3] += f.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = v[j] * alpha + bias[j];
+                if (ok && n > 0) store_run<4>(a, col0 + c, n0, n, v);
+            }
+        } else if (threadIdx.x < 128) {
+            for (int c = c0; c < c1 && col0 + c < a.q_rows; c += 8) {
+                float v[8] = {};
+                for (uint32_t r = 0; r < ranks; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += peer_load(base + 4 * ((c + j) * 128 + int(threadIdx.x)), r);
+                const int n = int(min(int64_t(8), a.q_rows - col0 - c));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * alpha + (j < n ? bias_at(a, col0 + c + j) : 0.0f);
+                if (ok && lane0 + threadIdx.x < a.p_rows) store_run<8>(a, lane0 + threadIdx.x, col0 + c, n, v);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its sums
+        fence_after();
+    }
+    if (!ok) atomicOr(&ep_op_status_word, 1u);
+    if (warp == 2) tmem_free(tmem, G::kColumns);
+}
+
+// A product without columns: out is the bias, or zero.
+__global__ void __launch_bounds__(256) bias_kernel(const MatmulArgs a, int64_t rows, int64_t cols) {
+    ms::wait_for_stream();
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * cols; i += int64_t(gridDim.x) * 256) {
+        const int64_t r = i / cols, c = i - r * cols;
+        const float v = bias_at(a, c);
+        const int64_t at = r * a.stride + c;
+        if (a.out_dtype == EP_F32) static_cast<float*>(a.out)[at] = v;
+        else if (a.out_dtype == EP_BF16) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+        else static_cast<__half*>(a.out)[at] = __float2half_rn(v);
+    }
+}
+
+// ---- host side -------------------------------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return EncodeTiled(nullptr);
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// Packed rows in boxes of 128 bytes x `box_rows`, swizzled; what lies outside reads as zeros.
+bool operand_map(CUtensorMap* map, const ep_fp4_tensor* t, int box_rows) {
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t row = cuuint64_t(op::fp4_row_bytes(t->cols));
+    const cuuint64_t dims[2] = {row, cuuint64_t(t->rows)}, strides[1] = {row};
+    const cuuint32_t box[2] = {128, cuuint32_t(box_rows)}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, t->data, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Sets the shared memory size of a variant's kernel, once per device.
+template <int NT, bool SWAP, bool NV>
+cudaError_t allow_smem(int dev) {
+    static std::atomic<bool> done[kMaxDevices];
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(fp4_matmul_kernel<NT, SWAP, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(Geo<NT, NV>::kSmem));
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
+template <int NT, bool SWAP, bool NV>
+int run_tiles(const ep_fp4_tensor* p, const ep_fp4_tensor* q, MatmulArgs a, int split, int dev, cudaStream_t st) {
+    using G = Geo<NT, NV>;
+    CUtensorMap p_map, q_map;
+    if (!operand_map(&p_map, p, 128) || !operand_map(&q_map, q, NT)) return set_error(EP_ERR_CUDA, "ep_fp4_matmul: tensor map");
+    a.p_scales = static_cast<const uint8_t*>(p->scales);
+    a.q_scales = static_cast<const uint8_t*>(q->scales);
+    a.p_rows = p->rows;
+    a.q_rows = q->rows;
+    a.p_tiles = int(op::div_up(p->rows, 128));
+    const int64_t grid = int64_t(a.p_tiles) * op::div_up(q->rows, NT) * split;
+    if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: too many tiles");
+    cudaError_t e = allow_smem<NT, SWAP, NV>(dev);
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(grid));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = G::kSmem;
+        cfg.stream = st;
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = unsigned(split);
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, fp4_matmul_kernel<NT, SWAP, NV>, p_map, q_map, a);
+    }
+    if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_matmul: ") + cudaGetErrorString(e));
+    return EP_OK;
+}
+
+template <bool NV>
+int matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int sms, int dev, cudaStream_t st) {
+    const int64_t m = a->rows, n = b->rows;
+    // CTAs of one tile: as many as fill two CTAs an SM, at most 8 and one stage each
+    auto split = [&](int64_t tiles) {
+        return int(std::max<int64_t>(1, std::min<int64_t>({8, args.steps, 2 * int64_t(sms) / std::max<int64_t>(1, tiles)})));
+    };
+    const int64_t n_tiles = op::div_up(n, 128);
+    if (m <= 16) return run_tiles<16, true, NV>(b, a, args, split(n_tiles), dev, st);
+    if (m <= 32) return run_tiles<32, true, NV>(b, a, args, split(n_tiles), dev, st);
+    if (m <= 64) return run_tiles<64, true, NV>(b, a, args, split(n_tiles), dev, st);
+    if (m <= 128) return run_tiles<128, true, NV>(b, a, args, split(n_tiles), dev, st);
+    const int64_t m_tiles = op::div_up(m, 128);
+    if (m_tiles * op::div_up(n, 256) >= sms) return run_tiles<256, false, NV>(a, b, args, 1, dev, st);
+    return run_tiles<128, false, NV>(a, b, args, split(m_tiles * n_tiles), dev, st);
+}
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const void* bias, const ep_tensor* out, void* stream) {
+    clear_error();
+    if (!a || !b || !out) return set_error(EP_ERR_ARG, "ep_fp4_matmul: NULL argument");
+    int rc = op::check_fp4(a, "ep_fp4_matmul");
+    if (rc == EP_OK) rc = op::check_fp4(b, "ep_fp4_matmul");
+    if (rc != EP_OK) return rc;
+    if (a->format != b->format) return set_error(EP_ERR_DTYPE, "ep_fp4_matmul: the operands differ in format");
+    if (a->cols != b->cols) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: the operands differ in columns");
+    const int es = op::elem_bytes(out->dtype);
+    if (es == 0) return set_error(EP_ERR_DTYPE, "ep_fp4_matmul: the output must be EP_BF16, EP_FP16 or EP_F32");
+    if (out->rows != a->rows || out->cols != b->rows) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: output shape");
+    if (bias && !op::aligned(bias, size_t(es))) return set_error(EP_ERR_ARG, "ep_fp4_matmul: the bias is misaligned");
+    const bool empty = out->rows == 0 || out->cols == 0;
+    if (!empty && (!out->data || !op::aligned(out->data, size_t(es)) || out->row_stride < out->cols))
+        return set_error(EP_ERR_ARG, "ep_fp4_matmul: bad output pointer or row stride");
+    int dev = 0, sms = 0;
+    rc = op::current_device(dev, sms);
+    if (rc != EP_OK) return rc;
+    if (a->device != dev || b->device != dev || out->device != dev)
+        return set_error(EP_ERR_ARG, "ep_fp4_matmul: a tensor is not on the current device");
+    if (empty) return EP_OK;
+    MatmulArgs args = {};
+    args.ga = a->tensor_scale;
+    args.gb = b->tensor_scale;
+    args.bias = bias;
+    args.out = out->data;
+    args.stride = out->row_stride;
+    args.out_dtype = out->dtype;
+    args.vec = op::aligned(out->data, 16) && (out->row_stride * es) % 16 == 0;
+    args.steps = int(op::div_up(a->cols, kStepK));
+    args.k64 = int(op::div_up(a->cols, 64));
+    args.scale_tiles = int(op::div_up(op::fp4_blocks(a->format, a->cols), 4));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (a->cols == 0) {
+        const int64_t n = out->rows * out->cols;
+        const cudaError_t e =
+            op::launch(bias_kernel, dim3(unsigned(std::min<int64_t>(op::div_up(n, 256), 8 * sms))), dim3(256), 0, st, args, out->rows, out->cols);
+        if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_matmul: ") + cudaGetErrorString(e));
+        return EP_OK;
+    }
+    return a->format == EP_NVFP4 ? matmul<true>(a, b, args, sms, dev, st) : matmul<false>(a, b, args, sms, dev, st);
+}
+
+extern "C" int ep_op_status(void* stream) {
+    clear_error();
+    uint32_t word = 0;
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&word, ep_op_status_word, sizeof(word));
+    const uint32_t zero = 0;
+    if (e == cudaSuccess && word) e = cudaMemcpyToSymbol(ep_op_status_word, &zero, sizeof(zero));
+    if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_op_status: ") + cudaGetErrorString(e));
+    if (word) return set_error(EP_ERR_CUDA, "a 4-bit product gave up waiting; its output is incomplete");
+    return EP_OK;
+}

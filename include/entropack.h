@@ -37,8 +37,12 @@ typedef enum {
     EP_FP16 = 2,
     EP_FP8_E4M3 = 3,  /* OCP E4M3 (bias 7, no infinities); outputs saturate to +-448 */
     EP_F32 = 4,
-    EP_INT8 = 5       /* two's complement integers; outputs round to nearest (ties to even) and
+    EP_INT8 = 5,      /* two's complement integers; outputs round to nearest (ties to even) and
                          saturate to [-128, 127] */
+    /* Microscaled 4-bit floating point, for ep_fp4_tensor and ep_cache only: E2M1 elements (a sign
+     * and 0, 0.5, 1, 1.5, 2, 3, 4 or 6), each block of a row sharing one scale. */
+    EP_MXFP4 = 6,     /* blocks of 32, power-of-two (E8M0) scales                             */
+    EP_NVFP4 = 7      /* blocks of 16, E4M3 scales, and one fp32 scale for the whole tensor   */
 } ep_dtype;
 
 typedef enum {
@@ -186,6 +190,162 @@ int ep_decompress_group(const ep_blob* const* blobs, const ep_tensor* outs, int 
  * EP_ERR_CUDA, EP_ERR_OOM.
  */
 int ep_decompress_fp8_rowscaled(const ep_blob* b, const ep_tensor* out, float* row_scale, void* stream);
+
+/* ---- microscaled 4-bit floating point ---------------------------------------------------------
+ *
+ * A 4-bit container beside the 8- and 16-bit ones: weights restored from a blob, or any matrix,
+ * quantised to it, and the product of two matrices in it on the 4-bit tensor cores.  (The method's
+ * pages compare against fixed-width 4-bit formats; the element and block formats are the OCP
+ * Microscaling specification's MXFP4, and its variant with blocks of 16 and E4M3 scales.)
+ *
+ * With amax the largest |v| of a block, and every rounding to nearest with ties to even:
+ *   EP_MXFP4  block scale q = 2^e, e = max(floor(log2 amax) - 2, -127), stored as the byte e + 127;
+ *   EP_NVFP4  block scale q = sb * g, sb = E4M3(amax / (6 g)) saturating at 448, stored as a byte;
+ *             g, the tensor scale, is a power of two: the smallest with amax(tensor) <= 2688 g, and
+ *             at least 2^-100, or the caller's.
+ *   element   E2M1(v / q), saturating at +-6; 0 where q = 0.
+ * These are the roundings of the exact quotients.  (g is a power of two so that a border between
+ * two codes is always a float and no quotient has to be formed in more than 24 bits; E4M3 scales
+ * span 18 binades, so fixing g to one of them costs at most one.)  A block that holds a NaN or an
+ * infinity gets a NaN scale and restores as NaNs; such values do not count towards g.
+ *
+ * Layout.  data: row r at r * row_bytes, row_bytes = 16 * ceil(cols / 32); two elements a byte, the
+ * even column in the low half; elements past the last column are 0.  scales: tiles of 512 bytes,
+ * one for 128 rows x 4 blocks, tile (i, j) at 512 * (i * ceil(blocks / 4) + j), blocks =
+ * ceil(cols / 32 or 16); the scale of row r and block k of a tile's own rows and blocks is its byte
+ * 16 * (r % 32) + 4 * (r / 32) + k; scales past the last row or block are 0. */
+#define EP_FP4_SCALE_FLOATS 1024 /* floats behind ep_fp4_tensor.tensor_scale */
+
+typedef struct {
+    void* data;          /* packed elements, 16-byte aligned                                   */
+    void* scales;        /* block scales, 16-byte aligned                                      */
+    float* tensor_scale; /* EP_FP4_SCALE_FLOATS floats in device memory; [0] is the tensor scale
+                            (1 for EP_MXFP4), the rest is work space of ep_fp4_quantize        */
+    int device;          /* CUDA device ordinal; host tensors are not accepted                 */
+    int format;          /* EP_MXFP4 or EP_NVFP4                                               */
+    int64_t rows;
+    int64_t cols;
+} ep_fp4_tensor;
+
+/* The sizes in bytes of the data and scales of a rows x cols tensor.  Returns EP_ERR_ARG (NULL
+ * pointer), EP_ERR_DTYPE (not a 4-bit format), EP_ERR_SHAPE (negative, or cols above 2^30). */
+int ep_fp4_sizes(int format, int64_t rows, int64_t cols, size_t* data_bytes, size_t* scale_bytes);
+
+/*
+ * Quantise a matrix.
+ *   x             device tensor on the current device, EP_BF16, EP_FP16 or EP_F32, any row stride.
+ *   out           same shape; data, scales (with their padding) and tensor_scale[0] are written.
+ *   tensor_scale  EP_NVFP4: 0 to take g from the data, or a power of two in [2^-100, 2^117] (one
+ *                 pass over x, no reduction); EP_MXFP4: 0.
+ *   stream        cudaStream_t as void*; asynchronous.
+ * No rows or no columns: nothing but tensor_scale[0] is written.  Returns EP_ERR_ARG (NULL or
+ * misaligned pointers, other device, bad stride or tensor_scale), EP_ERR_DTYPE, EP_ERR_SHAPE,
+ * EP_ERR_CUDA.
+ */
+int ep_fp4_quantize(const ep_tensor* x, const ep_fp4_tensor* out, double tensor_scale, void* stream);
+
+/* The values that a 4-bit tensor stands for, element * block scale * tensor scale, rounded once to
+ * out's type (EP_BF16, EP_FP16 or EP_F32; the product is formed in fp32 and exact there when the
+ * tensor scale is a power of two).  Same conventions and errors as ep_fp4_quantize. */
+int ep_fp4_dequantize(const ep_fp4_tensor* x, const ep_tensor* out, void* stream);
+
+/*
+ * Decompress a blob into the 4-bit container: ep_fp4_quantize of what ep_decompress writes in
+ * `work`'s element type (EP_BF16, EP_FP16 or EP_F32).
+ *   out           shaped like the blob.
+ *   tensor_scale  as for ep_fp4_quantize.
+ *   work          device tensor of the blob's shape for the restored weights, overwritten; it may be
+ *                 freed or reused on `stream` as soon as the call returns.
+ * Corrupt tiles are reported by ep_decode_status().  Errors as for ep_decompress and
+ * ep_fp4_quantize, found before anything is launched.
+ */
+int ep_decompress_fp4(const ep_blob* b, const ep_fp4_tensor* out, double tensor_scale, const ep_tensor* work,
+                      void* stream);
+
+/*
+ * The product out = a * transpose(b) + bias: out[i][j] = ga gb sum_k a[i][k] b[j][k] + bias[j], the
+ * form of a linear layer with activations a (tokens x in) and weights b (out x in).
+ *   a, b   4-bit tensors of one format and one number of columns, on the current device.
+ *   bias   NULL, or b->rows elements of out's type (aligned to their size).
+ *   out    a->rows x b->rows, EP_BF16, EP_FP16 or EP_F32, any row stride.
+ *   stream cudaStream_t as void*; one kernel, asynchronous, no work space.
+ * Sums are held in fp32, scaled, biased and then rounded once.  The order of a sum depends on the
+ * sizes only, so the same operands give the same bits.  With no columns the result is the bias (or
+ * 0).  out may not overlap the operands.  Errors as for ep_fp4_quantize; a kernel that gave up
+ * waiting for its copies reports it through ep_op_status().
+ */
+int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const void* bias, const ep_tensor* out, void* stream);
+
+/* ---- quantised key/value cache ----------------------------------------------------------------
+ *
+ * A paged cache of attention keys or values, quantised as it is written.  A slot is one position of
+ * one page, page * page_size + offset, and holds `heads` rows of head_dim elements, each row
+ * quantised by itself:
+ *   EP_FP8_E4M3  row scale s = the smallest power of two with amax <= 448 s, at least 2^-100 (fp32);
+ *                payload E4M3(v / s).  A power of two loses nothing in a floating-point payload
+ *                and makes every restored value exact in bf16 and fp32.
+ *   EP_INT8      s = fp32(amax / 127), 0 for rows with amax < 2^-100; payload the integer nearest
+ *                v / s (of the exact quotient, ties to even), 0 where s = 0.
+ *   EP_MXFP4, EP_NVFP4   the blocks of the 4-bit formats above along the row, with g = 1.
+ * A row (4-bit: a block) that holds a NaN or an infinity gets a NaN scale and restores as NaNs. */
+typedef struct {
+    void* data;      /* n_pages x page_size x heads x row bytes, 16-byte aligned; row bytes: head_dim for
+                        the 8-bit formats, 16 * ceil(head_dim / 32) for the 4-bit ones            */
+    void* scales;    /* n_pages x page_size x heads x (1 float, or ceil(head_dim / 32 or 16) bytes) */
+    int device;      /* CUDA device ordinal                                                       */
+    int format;      /* EP_FP8_E4M3, EP_INT8, EP_MXFP4 or EP_NVFP4                                */
+    int64_t n_pages;
+    int page_size;
+    int heads;
+    int head_dim;    /* 1 to 1024                                                                 */
+} ep_cache;
+
+/* Rows of attention heads: element (t, h, i) at data + (t * token_stride + h * head_stride + i). */
+typedef struct {
+    void* data;
+    int device;
+    int dtype;       /* EP_BF16, EP_FP16 or EP_F32 */
+    int64_t tokens;
+    int heads;
+    int head_dim;
+    int64_t token_stride, head_stride; /* elements, >= 0 */
+} ep_heads;
+
+/*
+ * Quantise tokens into their slots.
+ *   caches  n caches (1 or 2: keys and values) on the current device, of one geometry apart from
+ *           head_dim.
+ *   src     n sources; src[i] matches caches[i] in heads and head_dim, all have the same tokens.
+ *   slots   one int64 slot a token, device memory.  A token whose slot is negative or past the last
+ *           page is skipped (padding).  When a slot is named more than once, the last token that
+ *           names it is the one that is kept, in every cache.
+ *   stream  cudaStream_t as void*; asynchronous; one kernel per 4096 tokens, no work space.
+ * Other slots are left as they are.  Returns EP_ERR_ARG, EP_ERR_DTYPE, EP_ERR_SHAPE, EP_ERR_CUDA.
+ */
+int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n, const int64_t* slots, void* stream);
+
+/*
+ * Read sequences back: position p of sequence i, kept in page page_table[i][p / page_size], becomes
+ * token cu_seqlens[i] + p of out, rounded once to out's type.
+ *   caches      n caches (1 or 2) as for ep_cache_write.
+ *   out         n outputs with the same tokens; out[i] matches caches[i] in heads and head_dim; rows
+ *               may not overlap.
+ *   page_table  n_seqs x table_stride int32 in device memory, of which the first `pages_per_seq` of
+ *               a row are used.  A position whose page is negative, not below n_pages, or past
+ *               pages_per_seq reads as zeros.
+ *   cu_seqlens  n_seqs + 1 int32 in device memory, not decreasing, the first 0: where each sequence
+ *               starts in out, and the total.
+ *   stream      cudaStream_t as void*; asynchronous, one kernel.
+ * Tokens of out past the total are left as they are; sequences past out's tokens are cut off.
+ * Errors as for ep_cache_write.
+ */
+int ep_cache_read(const ep_cache* caches, const ep_heads* out, int n, const int32_t* page_table, int64_t table_stride,
+                  int64_t pages_per_seq, int n_seqs, const int32_t* cu_seqlens, void* stream);
+
+/* Synchronise `stream`, then read and clear the current device's status word of ep_fp4_matmul.
+ * Returns EP_OK, or EP_ERR_CUDA when a product since the last call gave up waiting for a copy or
+ * for the tensor cores (its output is then incomplete). */
+int ep_op_status(void* stream);
 
 /* Stored bits per element: 8 * (stored bytes including metadata) / (rows * cols)
  * ("EntroPack lattice compression", section "Encoding and reconstruction": the reported rate
