@@ -86,7 +86,7 @@ __device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int l
             s = pow2f(e);
             inv = pow2f(-e);
         } else {
-            s = amax >= 0x1p-100f ? __fdiv_rn(amax, 127.0f) : 0.0f;
+            s = amax >= 0x1p-100f ? __fmul_rn(amax, 1.0f / 127.0f) : 0.0f;
             inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
         }
         if (!fine) s = __int_as_float(0x7fc00000);

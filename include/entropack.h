@@ -284,8 +284,9 @@ int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const void* bi
  *   EP_FP8_E4M3  row scale s = the smallest power of two with amax <= 448 s, at least 2^-100 (fp32);
  *                payload E4M3(v / s).  A power of two loses nothing in a floating-point payload
  *                and makes every restored value exact in bf16 and fp32.
- *   EP_INT8      s = fp32(amax / 127), 0 for rows with amax < 2^-100; payload the integer nearest
- *                v / s (of the exact quotient, ties to even), 0 where s = 0.
+ *   EP_INT8      s = amax * (1 / 127), both factors and the product floats, 0 for rows with
+ *                amax < 2^-100; payload the integer nearest v / s (of the exact quotient, ties to
+ *                even), 0 where s = 0.
  *   EP_MXFP4, EP_NVFP4   the blocks of the 4-bit formats above along the row, with g = 1.
  * A row (4-bit: a block) that holds a NaN or an infinity gets a NaN scale and restores as NaNs. */
 typedef struct {
@@ -326,7 +327,8 @@ int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n, const int
 
 /*
  * Read sequences back: position p of sequence i, kept in page page_table[i][p / page_size], becomes
- * token cu_seqlens[i] + p of out, rounded once to out's type.
+ * token cu_seqlens[i] + p of out: payload * scale as a float, then rounded to out's type (only EP_INT8
+ * needs the first rounding).
  *   caches      n caches (1 or 2) as for ep_cache_write.
  *   out         n outputs with the same tokens; out[i] matches caches[i] in heads and head_dim; rows
  *               may not overlap.

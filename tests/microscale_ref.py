@@ -118,6 +118,6 @@ def cache_row(x, fmt):
         s = np.ldexp(1.0, e)
         p = e4m3(y / s[:, None])
     else:
-        s = np.where(top >= 2.0 ** -100, (top.astype(np.float32) / np.float32(127)).astype(np.float64), 0.0)
+        s = np.where(top >= 2.0 ** -100, (top.astype(np.float32) * (np.float32(1) / np.float32(127))).astype(np.float64), 0.0)
         p = np.where(s[:, None] > 0, np.rint(y / np.where(s > 0, s, 1.0)[:, None]), 0.0)
     return p, np.where(bad, np.nan, s)
