@@ -28,7 +28,7 @@ struct CacheView {
     int64_t token_stride, head_stride;
     int head_dim;
     int lanes;            // lanes of one row: a power of two, 8 elements each (4 x 8 above 256)
-    bool vec;             // rows are 16-byte aligned and whole chunks of 8
+    int width;            // alignment of its rows for load_raw8 and store8
 };
 
 struct WriteArgs {
@@ -36,7 +36,8 @@ struct WriteArgs {
     const int64_t* slots;
     int64_t n_slots;      // n_pages * page_size
     int64_t tokens;       // of this launch
-    int heads;
+    int n, heads;         // caches, and heads of each
+    float heads_inv;
     int per_block;        // tokens of one block
 };
 
@@ -46,7 +47,12 @@ struct ReadArgs {
     int64_t table_stride, pages_per_seq, n_pages, tokens;
     const int32_t* cu_seqlens;
     int n_seqs, page_size, heads;
+    float heads_inv;
 };
+
+// r / d for 0 <= r <= 2^20 and d_inv = 1.0f / d: (r + 1/2) / d is at least 1 / (2 d) away from an integer,
+// more than the product's rounding.
+__device__ __forceinline__ int quotient(int r, float d_inv) { return int((float(r) + 0.5f) * d_inv); }
 
 // ---- writing -----------------------------------------------------------------------------------
 
@@ -68,18 +74,63 @@ __device__ __forceinline__ int nearest_quotient(float v, float s, float inv) {
     return i;
 }
 
+// Eight int8 payload bytes.  Candidates from the reciprocal in pairs, rounded by adding 1.5 * 2^23 (the
+// integer is then the sum's low byte); only if a remainder is within 2^-20 of half a step, or above
+// it, the elements are settled one by one.
+template <int DT>
+__device__ __forceinline__ uint2 int8_payload(const Raw8<DT>& v, float s, float inv) {
+    constexpr float kMagic = 12582912.0f;
+    float2 y[4];
+    float worst = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = pair<DT>(v, i);
+        y[i] = fma2(x, both(inv), both(kMagic));
+        const float2 r = fma2(add2(y[i], both(-kMagic)), both(-s), x);
+        worst = fmaxf(worst, fmaxf(fabsf(r.x), fabsf(r.y)));
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = __byte_perm(__byte_perm(__float_as_uint(y[2 * i].x), __float_as_uint(y[2 * i].y), 0x0040),
+                           __byte_perm(__float_as_uint(y[2 * i + 1].x), __float_as_uint(y[2 * i + 1].y), 0x0040), 0x5410);
+    if (worst >= 0.5f * s * (1.0f - 0x1p-20f)) {
+        w[0] = w[1] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 x = pair<DT>(v, j / 2);
+            w[j / 4] |= uint32_t(nearest_quotient(j % 2 ? x.y : x.x, s, inv) & 0xff) << (8 * (j % 4));
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+template <int DT>
+__device__ __forceinline__ uint2 e4m3_payload(const Raw8<DT>& v, float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint16_t lo, hi;
+        const float2 a = mul2(pair<DT>(v, 2 * i), both(inv)), b = mul2(pair<DT>(v, 2 * i + 1), both(inv));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
+        w[i] = uint32_t(lo) | (uint32_t(hi) << 16);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
 // The payload (and by its first lane the scale) of one row, of which this lane holds chunks of 8
-// elements `lane`, `lane + lanes`, ...; v[k] are zeros past the row's end.
+// elements `lane`, `lane + lanes`, ...; they are zeros past the row's end.
 template <int DT, int FMT, int NC>
-__device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int lane, float (&v)[NC][8], bool live) {
+__device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int lane, const Raw8<DT>* v, bool live) {
     uint8_t* data = c.data + row * c.row_bytes;
     uint8_t* scales = c.scales + row * c.scale_bytes;
     if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
-        float amax = 0.0f;
+        uint32_t bits = 0;
 #pragma unroll
-        for (int k = 0; k < NC; ++k) amax = max_abs(amax, abs_max8(v[k]));
-        amax = lanes_max(amax, c.lanes);
-        const bool fine = is_finite(amax);
+        for (int k = 0; k < NC; ++k) bits = max(bits, abs_max8<DT>(v[k]));
+        bits = lanes_max(bits, c.lanes);
+        const bool fine = bits < AbsBits<DT>::kInf;
+        const float amax = abs_value<DT>(bits);
         float s, inv;
         if constexpr (FMT == EP_FP8_E4M3) {
             const int e = e4m3_row_exponent(amax);
@@ -87,7 +138,7 @@ __device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int l
             inv = pow2f(-e);
         } else {
             s = amax >= 0x1p-100f ? __fmul_rn(amax, 1.0f / 127.0f) : 0.0f;
-            inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
+            inv = s > 0.0f ? reciprocal_near(s) : 0.0f;
         }
         if (!fine) s = __int_as_float(0x7fc00000);
         if (!live) return;
@@ -96,27 +147,17 @@ __device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int l
         for (int k = 0; k < NC; ++k) {
             const int at = 8 * (lane + k * c.lanes);
             if (at >= c.head_dim) break;
-            uint32_t w[2] = {0, 0};
+            uint2 w = make_uint2(0, 0);
             if (fine && inv > 0.0f) {
-                if constexpr (FMT == EP_FP8_E4M3) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint16_t two;
-                        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(v[k][2 * j + 1] * inv), "f"(v[k][2 * j] * inv));
-                        w[j / 2] |= uint32_t(two) << (16 * (j % 2));
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        w[j / 4] |= uint32_t(nearest_quotient(v[k][j], s, inv) & 0xff) << (8 * (j % 4));
-                }
+                if constexpr (FMT == EP_FP8_E4M3) w = e4m3_payload<DT>(v[k], inv);
+                else w = int8_payload<DT>(v[k], s, inv);
             }
             if (c.head_dim % 8 == 0) {  // 8-byte aligned: the pool is, and so is every row
-                *reinterpret_cast<uint2*>(data + at) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2*>(data + at) = w;
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (at + j < c.head_dim) data[at + j] = uint8_t(w[j / 4] >> (8 * (j % 4)));
+                    if (at + j < c.head_dim) data[at + j] = uint8_t((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
             }
         }
     } else {
@@ -124,8 +165,7 @@ __device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int l
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
             const int chunk = lane + k * c.lanes, at = 8 * chunk;
-            const float amax = lanes_max(abs_max8(v[k]), NV ? 2 : 4);
-            const Block b = block_scale<NV>(amax, 1.0f, 1.0f);
+            const Block b = block_scale<DT, NV>(lanes_max(abs_max8<DT>(v[k]), NV ? 2 : 4), 1.0f, 1.0f);
             const uint32_t codes = quantize8<DT, NV>(v[k], b);
             if (!live || at / 2 >= c.row_bytes) continue;
             *reinterpret_cast<uint32_t*>(data + at / 2) = codes;
@@ -134,16 +174,17 @@ __device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int l
     }
 }
 
-// A block takes a few tokens, all heads.  First it looks through the later tokens of the launch for
-// its own slots: a token whose slot is named again later is dropped, so that payload and scale of a
-// slot always come from one token (launches of one call follow each other, the later wins).
+// A block takes a few tokens, all heads of every cache.  First it looks through the later tokens of the
+// launch for its own slots: a token whose slot is named again later is dropped, so that payload and
+// scale of a slot always come from one token (launches of one call follow each other, the later wins).
+// Rows then go in batches, whose loads are all on their way before the first is used.
 template <int DT, int FMT, int NC>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteArgs a) {
     using T = typename Elem<DT>::T;
+    constexpr int kBatch = NC == 1 ? (DT == EP_F32 ? 2 : 4) : 1;
     __shared__ int64_t slot[kMaxWriteTokens];
     __shared__ int dropped[kMaxWriteTokens];
     wait_for_stream();
-    const CacheView& c = a.c[blockIdx.y];
     const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
     const int n = int(min(int64_t(a.per_block), a.tokens - t0));
     if (int(threadIdx.x) < n) {
@@ -164,70 +205,83 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a
         }
     __syncthreads();
 
-    const int lanes = c.lanes, lane = threadIdx.x % lanes;
-    const int step = kThreads / lanes, rows = n * a.heads;
-    // every lane of a warp stays in the loop: rows past the end are read as zeros and not written
-    for (int base = 0; base < rows; base += step) {
-        const int r = base + int(threadIdx.x) / lanes;
-        const int i = min(r / a.heads, n - 1), h = r % a.heads;
-        const bool live = r < rows && slot[i] >= 0 && !dropped[i];
-        const T* src = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride;
-        float v[NC][8];
+    const int rows = n * a.heads;
+    for (int ci = 0; ci < a.n; ++ci) {
+        const CacheView& c = a.c[ci];
+        const int lane = threadIdx.x % c.lanes, step = kThreads / c.lanes;
+        // every lane of a warp stays in the loop: rows past the end are zeros and not written
+        for (int base = int(threadIdx.x) / c.lanes; base - int(threadIdx.x) / c.lanes < rows; base += kBatch * step) {
+            Raw8<DT> v[kBatch][NC];
+            int64_t at[kBatch];
 #pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int at = 8 * (lane + k * lanes);
-            const int m = live ? max(0, min(8, c.head_dim - at)) : 0;
-            if (c.vec && m == 8) raw_to_float8<DT>(load_raw8<DT>(src + at), v[k]);
-            else load_some<DT>(src + at, m, v[k]);
+            for (int u = 0; u < kBatch; ++u) {
+                const int r = base + u * step;
+                const int i = min(quotient(r, a.heads_inv), n - 1), h = r - i * a.heads;
+                const bool live = r < rows && slot[i] >= 0 && !dropped[i];
+                at[u] = live ? slot[i] * a.heads + h : -1;
+                const T* src = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride;
+#pragma unroll
+                for (int k = 0; k < NC; ++k) {
+                    const int e = 8 * (lane + k * c.lanes);
+                    v[u][k] = load_raw8<DT>(src + e, live ? max(0, min(8, c.head_dim - e)) : 0, c.width);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) write_row<DT, FMT, NC>(c, max(at[u], int64_t(0)), lane, v[u], at[u] >= 0);
         }
-        write_row<DT, FMT, NC>(c, slot[i] * a.heads + h, lane, v, live);
     }
 }
 
 // ---- reading -----------------------------------------------------------------------------------
 
-template <int DT, int FMT>
-__device__ __forceinline__ void read_chunk(const CacheView& c, int64_t row, int chunk, typename Elem<DT>::T* dst) {
-    const int at = 8 * chunk;
-    if (at >= c.head_dim) return;
-    float v[8];
-    if (row < 0) {  // no such page
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    } else {
-        const uint8_t* data = c.data + row * c.row_bytes;
-        const uint8_t* scales = c.scales + row * c.scale_bytes;
-        if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
-            uint32_t w[2] = {0, 0};
-            if (c.head_dim % 8 == 0) {
-                const uint2 u = *reinterpret_cast<const uint2*>(data + at);
-                w[0] = u.x;
-                w[1] = u.y;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (at + j < c.head_dim) w[j / 4] |= uint32_t(data[at + j]) << (8 * (j % 4));
-            }
-            const float s = *reinterpret_cast<const float*>(scales);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t two = (w[j / 2] >> (16 * (j % 2))) & 0xffffu;
-                const float2 f = FMT == EP_FP8_E4M3
-                                     ? e4m3x2_value(two)
-                                     : make_float2(float(int8_t(two & 0xff)), float(int8_t(two >> 8)));
-                v[2 * j] = f.x * s;
-                v[2 * j + 1] = f.y * s;
-            }
+// A chunk of 8 elements as it lies in the cache, and its scale.
+template <int FMT>
+struct Chunk {
+    uint2 w;
+    float s;
+};
+template <int FMT>
+__device__ __forceinline__ Chunk<FMT> load_chunk(const CacheView& c, int64_t row, int chunk) {
+    Chunk<FMT> q;
+    q.w = make_uint2(0, 0);
+    q.s = 0.0f;
+    if (row < 0) return q;  // no such page
+    const uint8_t* data = c.data + row * c.row_bytes;
+    const uint8_t* scales = c.scales + row * c.scale_bytes;
+    if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
+        const int at = 8 * chunk;
+        if (c.head_dim % 8 == 0) {
+            q.w = *reinterpret_cast<const uint2*>(data + at);
         } else {
-            constexpr bool NV = FMT == EP_NVFP4;
-            e2m1_values8(*reinterpret_cast<const uint32_t*>(data + at / 2), v);
-            const float s = scale_value<NV>(scales[chunk / (NV ? 2 : 4)]);
+            uint32_t w[2] = {0, 0};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= s;
+            for (int j = 0; j < 8; ++j)
+                if (at + j < c.head_dim) w[j / 4] |= uint32_t(data[at + j]) << (8 * (j % 4));
+            q.w = make_uint2(w[0], w[1]);
         }
+        q.s = *reinterpret_cast<const float*>(scales);
+    } else {
+        q.w.x = *reinterpret_cast<const uint32_t*>(data + 4 * chunk);
+        q.s = scale_value<FMT == EP_NVFP4>(scales[chunk / (FMT == EP_NVFP4 ? 2 : 4)]);
     }
-    if (c.vec) store8<DT>(dst + at, v);
-    else store_some<DT>(dst + at, min(8, c.head_dim - at), v);
+    return q;
+}
+template <int FMT>
+__device__ __forceinline__ void chunk_values(const Chunk<FMT>& q, float* v) {
+    if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t two = ((j < 2 ? q.w.x : q.w.y) >> (16 * (j % 2))) & 0xffffu;
+            const float2 f = FMT == EP_FP8_E4M3 ? e4m3x2_value(two)
+                                                : make_float2(float(int8_t(two & 0xff)), float(int8_t(two >> 8)));
+            v[2 * j] = f.x * q.s;
+            v[2 * j + 1] = f.y * q.s;
+        }
+    } else {
+        e2m1_values8(q.w.x, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= q.s;
+    }
 }
 
 // The last sequence that starts at or before token t.
@@ -241,10 +295,10 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seqs, int64_
     return lo;
 }
 
-// A block takes 16 tokens of the output, all heads: finds their slots, then its threads take chunks
-// of 8 elements.
+// A block takes 16 tokens of one output, all heads: finds their slots, then reads rows in batches,
+// whose loads are all on their way before the first is used.
 template <int DT, int FMT>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
     using T = typename Elem<DT>::T;
     __shared__ int32_t starts[kSharedSeqs + 1];
     __shared__ int64_t slot[kReadTokens];  // -1: zeros, -2: past the sequences
@@ -273,28 +327,42 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadArgs a) 
         slot[threadIdx.x] = s;
     }
     __syncthreads();
-    const int chunks = (c.head_dim + 7) / 8, per_token = a.heads * chunks;
-    for (int i = threadIdx.x; i < n * per_token; i += kThreads) {
-        const int t = i / per_token, h = i % per_token / chunks, chunk = i % chunks;
-        if (slot[t] == -2) continue;
-        T* dst = static_cast<T*>(c.heads) + (t0 + t) * c.token_stride + h * c.head_stride;
-        read_chunk<DT, FMT>(c, slot[t] < 0 ? -1 : slot[t] * a.heads + h, chunk, dst);
-    }
+    constexpr int kBatch = 4;
+    const int chunks = (c.head_dim + 7) / 8, rows = n * a.heads, step = kThreads / c.lanes;
+    for (int chunk = threadIdx.x % c.lanes; chunk < chunks; chunk += c.lanes)
+        for (int base = int(threadIdx.x) / c.lanes; base < rows; base += kBatch * step) {
+            Chunk<FMT> q[kBatch];
+            int64_t at[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int r = min(base + u * step, rows - 1);
+                const int t = quotient(r, a.heads_inv), h = r - t * a.heads;
+                at[u] = base + u * step < rows && slot[t] != -2 ? (t0 + t) * c.token_stride + h * c.head_stride + 8 * chunk : -1;
+                q[u] = load_chunk<FMT>(c, slot[t] < 0 ? -1 : slot[t] * a.heads + h, chunk);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (at[u] < 0) continue;
+                float v[8];
+                chunk_values<FMT>(q[u], v);
+                store8<DT>(static_cast<T*>(c.heads) + at[u], min(8, c.head_dim - 8 * chunk), c.width, v);
+            }
+        }
 }
 
 // ---- host side -----------------------------------------------------------------------------------
 template <int DT, int FMT>
-cudaError_t launch_write(const WriteArgs& w, int n, bool wide, cudaStream_t st) {
-    const dim3 grid(unsigned(op::div_up(w.tokens, w.per_block)), unsigned(n));
+cudaError_t launch_write(const WriteArgs& w, bool wide, cudaStream_t st) {
+    const dim3 grid(unsigned(op::div_up(w.tokens, w.per_block)));
     return op::launch(wide ? cache_write_kernel<DT, FMT, 4> : cache_write_kernel<DT, FMT, 1>, grid, dim3(kThreads), 0, st, w);
 }
 template <int DT>
-cudaError_t write_as(int fmt, const WriteArgs& w, int n, bool wide, cudaStream_t st) {
+cudaError_t write_as(int fmt, const WriteArgs& w, bool wide, cudaStream_t st) {
     switch (fmt) {
-        case EP_FP8_E4M3: return launch_write<DT, EP_FP8_E4M3>(w, n, wide, st);
-        case EP_INT8: return launch_write<DT, EP_INT8>(w, n, wide, st);
-        case EP_MXFP4: return launch_write<DT, EP_MXFP4>(w, n, wide, st);
-        default: return launch_write<DT, EP_NVFP4>(w, n, wide, st);
+        case EP_FP8_E4M3: return launch_write<DT, EP_FP8_E4M3>(w, wide, st);
+        case EP_INT8: return launch_write<DT, EP_INT8>(w, wide, st);
+        case EP_MXFP4: return launch_write<DT, EP_MXFP4>(w, wide, st);
+        default: return launch_write<DT, EP_NVFP4>(w, wide, st);
     }
 }
 template <int DT, int FMT>
@@ -347,7 +415,7 @@ int make_views(const ep_cache* caches, const ep_heads* h, int n, const char* who
         v.head_dim = c.head_dim;
         v.lanes = 4;  // a 4-bit block is 2 or 4 lanes
         while (v.lanes < 32 && 8 * v.lanes < c.head_dim) v.lanes *= 2;
-        v.vec = c.head_dim % 8 == 0 && op::aligned(x.data, 16) && (x.token_stride * es) % 16 == 0 && (x.head_stride * es) % 16 == 0;
+        v.width = op::access_width(x.data, x.token_stride * es, x.head_stride * es);
     }
     return EP_OK;
 }
@@ -382,7 +450,9 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
     const bool wide = src[0].head_dim > 256 || (n == 2 && src[1].head_dim > 256);
     const int es = op::elem_bytes(src[0].dtype);
     w.n_slots = caches[0].n_pages * caches[0].page_size;
+    w.n = n;
     w.heads = caches[0].heads;
+    w.heads_inv = 1.0f / float(w.heads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     for (int64_t t0 = 0; t0 < tokens; t0 += kLaunchTokens) {
         WriteArgs part = w;
@@ -391,10 +461,10 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
         for (int i = 0; i < n; ++i)
             part.c[i].heads = static_cast<uint8_t*>(w.c[i].heads) + t0 * w.c[i].token_stride * es;
         // few tokens are spread over as many blocks as there are SMs
-        part.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxWriteTokens, part.tokens * n / (2 * sms))));
-        const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, n, wide, st)
-                              : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, n, wide, st)
-                                                        : write_as<EP_F32>(caches[0].format, part, n, wide, st);
+        part.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxWriteTokens, part.tokens / (2 * sms))));
+        const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, wide, st)
+                              : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, wide, st)
+                                                        : write_as<EP_F32>(caches[0].format, part, wide, st);
         if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_cache_write: ") + cudaGetErrorString(e));
     }
     return EP_OK;
@@ -423,6 +493,7 @@ extern "C" int ep_cache_read(const ep_cache* caches, const ep_heads* out, int n,
     r.n_seqs = n_seqs;
     r.page_size = caches[0].page_size;
     r.heads = caches[0].heads;
+    r.heads_inv = 1.0f / float(r.heads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = out[0].dtype == EP_BF16   ? read_as<EP_BF16>(caches[0].format, r, n, st)
                           : out[0].dtype == EP_FP16 ? read_as<EP_FP16>(caches[0].format, r, n, st)

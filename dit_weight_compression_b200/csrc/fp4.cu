@@ -32,69 +32,53 @@ struct QuantArgs {
     float fixed;      // > 0: the tensor scale
     int partials;     // > 0: its maxima are in tensor_scale[1 ..]; 0 and no fixed scale: each block
                       // looks at all of x
-    bool vec;         // rows are 16-byte aligned
+    int width;        // alignment of the rows for load_raw8
+    bool backwards;   // take the last rows first
 };
 
-// Eight elements from column c of a row, zeros past the last column.
+// The largest finite |v| of eight, as bits.
 template <int DT>
-__device__ __forceinline__ void load_row8(const typename Elem<DT>::T* row, int64_t c, int64_t cols, bool vec, float* v) {
-    if (vec && c + 8 <= cols) raw_to_float8<DT>(load_raw8<DT>(row + c), v);
-    else load_some<DT>(row + c, int(max(int64_t(0), min(int64_t(8), cols - c))), v);
-}
-
-// The largest finite |v| of eight.
-__device__ __forceinline__ float finite_max8(const float* v) {
-    float m = abs_max8(v);
-    if (!is_finite(m)) {
-        m = 0.0f;
+__device__ __forceinline__ uint32_t finite_max8(const Raw8<DT>& r) {
+    uint32_t m = abs_max8(r);
+    if (m >= AbsBits<DT>::kInf) {
+        m = 0;
+        constexpr uint32_t kMask = DT == EP_F32 ? 0x7fffffffu : 0x7fffu;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (is_finite(fabsf(v[j]))) m = fmaxf(m, fabsf(v[j]));
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w = (DT == EP_F32 ? r.w[j] : r.w[j / 2] >> (16 * (j % 2))) & kMask;
+            if (w < AbsBits<DT>::kInf) m = max(m, w);
+        }
     }
     return m;
 }
 
 // The largest of a block's threads, in all of them.
-__device__ __forceinline__ float block_max(float m, float* smem) {
+__device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* smem) {
     m = lanes_max(m, 32);
     if (threadIdx.x % 32 == 0) smem[threadIdx.x / 32] = m;
     __syncthreads();
-    m = smem[threadIdx.x % (kThreads / 32)];
-    m = lanes_max(m, kThreads / 32);
-    return m;
+    return lanes_max(smem[threadIdx.x % (kThreads / 32)], kThreads / 32);
 }
 
-// Chunks of eight elements `first`, `first + step`, ... of x, row by row.
+// Chunks of eight elements `first`, `first + step`, ... of x, row by row; four in flight.
 template <int DT>
-__device__ __forceinline__ float max_of_chunks(const QuantArgs& a, int64_t first, int64_t step) {
+__device__ __forceinline__ uint32_t max_of_chunks(const QuantArgs& a, int64_t first, int64_t step) {
     using T = typename Elem<DT>::T;
     const int64_t per_row = (a.cols + 7) / 8, n = a.rows * per_row;
     const T* x = static_cast<const T*>(a.x);
-    float m = 0.0f;
-    if (a.vec && a.cols % 8 == 0) {
-        // eight loads in flight; rows without gaps need no division
-        const bool flat = a.stride == a.cols;
-        for (int64_t i = first; i < n; i += 4 * step) {
-            Raw8<DT> r[4];
+    const bool flat = a.stride == a.cols && a.cols % 8 == 0;  // rows without gaps need no division
+    uint32_t m = 0;
+    for (int64_t i = first; i < n; i += 4 * step) {
+        Raw8<DT> r[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int64_t j = min(i + k * step, n - 1);
-                r[k] = load_raw8<DT>(flat ? x + 8 * j : x + (j / per_row) * a.stride + 8 * (j % per_row));
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float v[8];
-                raw_to_float8<DT>(r[k], v);
-                m = fmaxf(m, finite_max8(v));
-            }
+        for (int k = 0; k < 4; ++k) {
+            const int64_t j = i + k * step;
+            const int64_t row = flat || j >= n ? 0 : j / per_row, c = 8 * (j - row * per_row);
+            const int have = j >= n ? 0 : flat ? 8 : int(min(int64_t(8), a.cols - c));
+            r[k] = load_raw8<DT>(x + row * a.stride + c, have, a.width);
         }
-        return m;
-    }
-    for (int64_t i = first; i < n; i += step) {
-        float v[8];
-        const int64_t row = i / per_row;
-        load_row8<DT>(x + row * a.stride, 8 * (i - row * per_row), a.cols, a.vec, v);
-        m = fmaxf(m, finite_max8(v));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = max(m, finite_max8<DT>(r[k]));
     }
     return m;
 }
@@ -102,68 +86,72 @@ __device__ __forceinline__ float max_of_chunks(const QuantArgs& a, int64_t first
 // First pass over x for a tensor scale: block i's maximum goes to tensor_scale[1 + i].
 template <int DT>
 __global__ void __launch_bounds__(kThreads) amax_kernel(const QuantArgs a) {
-    __shared__ float smem[kThreads / 32];
+    __shared__ uint32_t smem[kThreads / 32];
     wait_for_stream();
-    const float m = block_max(
+    const uint32_t m = block_max(
         max_of_chunks<DT>(a, int64_t(blockIdx.x) * kThreads + threadIdx.x, int64_t(gridDim.x) * kThreads), smem);
-    if (threadIdx.x == 0) a.tensor_scale[1 + blockIdx.x] = m;
+    if (threadIdx.x == 0) a.tensor_scale[1 + blockIdx.x] = abs_value<DT>(m);
 }
 
-// One pass: a block reads its 128 x 128 elements (8 loads a thread in flight), forms the block
-// scales among 2 or 4 neighbouring threads, writes 4 bytes of codes a thread and its scale tiles.
+// One pass: a block reads its 128 x 128 elements (8 loads of 16 bytes a thread in flight), forms the
+// block scales among 2 or 4 neighbouring threads, writes 4 bytes of codes a thread and its scale tiles.
 template <int DT, bool NV>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) quantize_kernel(const QuantArgs a) {
     using T = typename Elem<DT>::T;
-    __shared__ float red[kThreads / 32];
+    constexpr int kBatch = DT == EP_F32 ? kPasses / 2 : kPasses;
+    __shared__ uint32_t red[kThreads / 32];
     __shared__ __align__(16) uint8_t sc[NV ? 1024 : 512];
     wait_for_stream();
-    const int64_t row0 = int64_t(blockIdx.x / a.col_tiles) * kTileRows;
-    const int64_t col = int64_t(blockIdx.x % a.col_tiles) * kTileCols + 8 * (threadIdx.x % 16);
+    const uint32_t block = a.backwards ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    const uint32_t row_tile = block / uint32_t(a.col_tiles), col_tile = block - row_tile * uint32_t(a.col_tiles);
+    const int64_t row0 = int64_t(row_tile) * kTileRows;
+    const int64_t col = int64_t(col_tile) * kTileCols + 8 * (threadIdx.x % 16);
     const int sub = threadIdx.x / 16;
-    const T* x = static_cast<const T*>(a.x) + (row0 + sub) * a.stride;
-
-    float v[kPasses][8];
+    const int rows = int(min(int64_t(kTileRows), a.rows - row0));
     const int n = int(max(int64_t(0), min(int64_t(8), a.cols - col)));
+    const T* x = static_cast<const T*>(a.x) + (row0 + sub) * a.stride + col;
+    uint8_t* data = a.data + (row0 + sub) * a.row_bytes + col / 2;
+    const int k = (threadIdx.x % 16) / (NV ? 2 : 4);  // the scale block's column in this tile
+    const bool scales = threadIdx.x % (NV ? 2 : 4) == 0, codes_in = col < 2 * a.row_bytes;
+
+    float g = 1.0f, g_inv = 1.0f;
+    Raw8<DT> v[kBatch];
 #pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-        const bool in = row0 + sub + p * kPassRows < a.rows;
-        const T* src = x + int64_t(p) * kPassRows * a.stride + col;
-        if (a.vec && n == 8 && in) raw_to_float8<DT>(load_raw8<DT>(src), v[p]);
-        else load_some<DT>(src, in ? n : 0, v[p]);
-    }
-    float g = 1.0f;
-    if constexpr (NV) {
-        if (a.fixed > 0.0f) {
-            g = a.fixed;
-        } else {
-            float m = 0.0f;
-            if (a.partials > 0)
-                for (int i = threadIdx.x; i < a.partials; i += kThreads) m = fmaxf(m, a.tensor_scale[1 + i]);
-            else
-                m = max_of_chunks<DT>(a, threadIdx.x, kThreads);
-            g = tensor_scale_of(block_max(m, red));
+    for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+#pragma unroll
+        for (int p = 0; p < kBatch; ++p)
+            v[p] = load_raw8<DT>(x + int64_t(p0 + p) * kPassRows * a.stride, sub + (p0 + p) * kPassRows < rows ? n : 0, a.width);
+        if (NV && p0 == 0) {
+            if (a.fixed > 0.0f) {
+                g = a.fixed;
+            } else {
+                uint32_t m = 0;
+                if (a.partials > 0) {
+                    for (int i = threadIdx.x; i < a.partials; i += kThreads) m = max(m, __float_as_uint(a.tensor_scale[1 + i]));
+                    g = tensor_scale_of(__uint_as_float(block_max(m, red)));
+                } else {
+                    m = max_of_chunks<DT>(a, threadIdx.x, kThreads);
+                    g = tensor_scale_of(abs_value<DT>(block_max(m, red)));
+                }
+            }
+            g_inv = pow2f(-log2_floor(g));
+        }
+#pragma unroll
+        for (int p = 0; p < kBatch; ++p) {
+            const int r = sub + (p0 + p) * kPassRows;
+            const Block b = block_scale<DT, NV>(lanes_max(abs_max8<DT>(v[p]), NV ? 2 : 4), g, g_inv);
+            const uint32_t codes = quantize8<DT, NV>(v[p], b);
+            const bool in = r < rows;
+            if (in && codes_in) *reinterpret_cast<uint32_t*>(data + int64_t(p0 + p) * kPassRows * a.row_bytes) = codes;
+            if (scales) sc[(k / 4) * 512 + 16 * (r % 32) + 4 * (r / 32) + k % 4] = in && n > 0 ? b.byte : 0;
         }
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.tensor_scale[0] = g;
-    const float g_inv = 1.0f / g;
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-        const int r = sub + p * kPassRows;
-        const float amax = lanes_max(abs_max8(v[p]), NV ? 2 : 4);
-        const Block b = block_scale<NV>(amax, g, g_inv);
-        const uint32_t codes = quantize8<DT, NV>(v[p], b);
-        const bool in = row0 + r < a.rows;
-        if (in && col < 2 * a.row_bytes)
-            *reinterpret_cast<uint32_t*>(a.data + (row0 + r) * a.row_bytes + col / 2) = codes;
-        const int k = (threadIdx.x % 16) / (NV ? 2 : 4);  // the block's column in this tile
-        if (threadIdx.x % (NV ? 2 : 4) == 0)
-            sc[(k / 4) * 512 + 16 * (r % 32) + 4 * (r / 32) + k % 4] = in && col < a.cols ? b.byte : 0;
-    }
     __syncthreads();
-    const int64_t st = int64_t(blockIdx.x % a.col_tiles) * (NV ? 2 : 1);
-    const int tiles = int(min(int64_t(NV ? 2 : 1), a.scale_tiles - st));
+    const int st = int(col_tile) * (NV ? 2 : 1);
+    const int tiles = min(NV ? 2 : 1, a.scale_tiles - st);
     if (int(threadIdx.x) < 32 * tiles)
-        reinterpret_cast<uint4*>(a.scales + ((row0 / kTileRows) * a.scale_tiles + st) * 512)[threadIdx.x] =
+        reinterpret_cast<uint4*>(a.scales + (int64_t(row_tile) * a.scale_tiles + st) * 512)[threadIdx.x] =
             reinterpret_cast<const uint4*>(sc)[threadIdx.x];
 }
 
@@ -179,7 +167,7 @@ struct DequantArgs {
     void* out;
     int64_t stride, rows, cols, row_bytes;
     int col_tiles, scale_tiles;
-    bool vec;
+    int width;        // alignment of out's rows for store8
 };
 
 // The same blocks backwards: scale tiles to shared memory, 4 bytes of codes a thread, 8 elements out.
@@ -218,8 +206,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = v[j] * s * g;
         T* dst = static_cast<T*>(a.out) + (row0 + r) * a.stride + col;
-        if (a.vec && n == 8) store8<DT>(dst, v);
-        else store_some<DT>(dst, n, v);
+        store8<DT>(dst, n, a.width, v);
     }
 }
 
@@ -302,13 +289,14 @@ int quantize(const ep_tensor* x, const ep_fp4_tensor* out, double tensor_scale, 
         q.col_tiles = int(op::div_up(x->cols, kTileCols));
         q.scale_tiles = int(op::div_up(op::fp4_blocks(out->format, x->cols), 4));
         q.fixed = float(tensor_scale);
-        q.vec = op::aligned(x->data, 16) && (x->row_stride * es) % 16 == 0;
+        q.width = op::access_width(x->data, x->row_stride * es);
         const int64_t grid = op::div_up(x->rows, kTileRows) * q.col_tiles;
         if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, std::string(who) + ": the matrix is too large");
         int amax_grid = 0;
         if (nv && tensor_scale == 0.0 && x->rows * x->cols * es > kSearchBytes) {
             amax_grid = int(std::min<int64_t>({kMaxPartials, 4 * int64_t(sms), op::div_up(x->rows * x->cols, 8 * 4 * kThreads)}));
             q.partials = amax_grid;
+            q.backwards = true;  // what the first pass read last is still in L2
         }
         e = x->dtype == EP_BF16   ? launch_quantize<EP_BF16>(q, nv, grid, amax_grid, st)
             : x->dtype == EP_FP16 ? launch_quantize<EP_FP16>(q, nv, grid, amax_grid, st)
@@ -367,7 +355,7 @@ extern "C" int ep_fp4_dequantize(const ep_fp4_tensor* x, const ep_tensor* out, v
     q.row_bytes = op::fp4_row_bytes(x->cols);
     q.col_tiles = int(op::div_up(x->cols, kTileCols));
     q.scale_tiles = int(op::div_up(op::fp4_blocks(x->format, x->cols), 4));
-    q.vec = op::aligned(out->data, 16) && (out->row_stride * op::elem_bytes(out->dtype)) % 16 == 0;
+    q.width = op::access_width(out->data, out->row_stride * op::elem_bytes(out->dtype));
     const int64_t grid = op::div_up(x->rows, kTileRows) * q.col_tiles;
     if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_dequantize: the tensor is too large");
     const bool nv = x->format == EP_NVFP4;

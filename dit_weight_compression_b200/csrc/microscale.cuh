@@ -5,11 +5,15 @@
 // at most four significant bits (a power of two, or an E4M3 value times a power of two): the border
 // between two codes, m * q with m of three bits, is then a float itself.
 //   * q a power of two: v / q is a float, nothing is rounded before the code.
-//   * fp32 elements, other q: the IEEE quotient falls on a border only if v does, because two
-//     different floats differ by more than the division's rounding (2^-24 relative).
+//   * fp32 elements, other q: the correctly rounded quotient (Markstein: an approximate quotient, its
+//     exact remainder, one correction) falls on a border only if v does, because two different
+//     floats differ by more than that rounding (2^-24 relative).
 //   * bf16 and fp16 elements, other q: v has at most 11 bits, so v / q is on a border m or at least
 //     m * 2^-11 >= 2^-13 away from it.  One fma, v * (1/q) + 384, rounds to a multiple of 2^-15:
-//     the reciprocal's error (2^-24) cannot take a value over a border, and borders come out exact.
+//     the reciprocal's error (2^-22) cannot take a value over a border, and borders come out exact.
+// The elements go in pairs through the packed fp32 instructions, and the largest of 16-bit elements is
+// found on their bits, two at a time: a block costs about 7 instructions an element less than one by
+// one, and the quantiser is bound by its loads instead of by issue.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,73 +41,113 @@ struct Elem<EP_FP16> { using T = __half; };
 template <>
 struct Elem<EP_F32> { using T = float; };
 
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_float(float v) { return v; }
-
-// Eight neighbouring elements as loaded, and as floats.
+// Eight neighbouring elements as loaded.
 template <int DT>
-struct Raw8 { uint4 u[DT == EP_F32 ? 2 : 1]; };
+struct Raw8 { uint32_t w[DT == EP_F32 ? 8 : 4]; };
 
 template <int DT>
-__device__ __forceinline__ Raw8<DT> load_raw8(const typename Elem<DT>::T* p) {
+__device__ __forceinline__ Raw8<DT> zero_raw8() {
     Raw8<DT> r;
 #pragma unroll
-    for (int i = 0; i < (DT == EP_F32 ? 2 : 1); ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (uint32_t& w : r.w) w = 0;
     return r;
 }
 
+// n (0 to 8) elements from p on, zeros behind them.  `width`: the alignment of p in bytes, 16, 8 or 4;
+// anything less goes element by element.
 template <int DT>
-__device__ __forceinline__ void raw_to_float8(const Raw8<DT>& r, float* v) {
-    if constexpr (DT == EP_F32) {
+__device__ __forceinline__ Raw8<DT> load_raw8(const typename Elem<DT>::T* p, int n, int width) {
+    constexpr int W = DT == EP_F32 ? 8 : 4;
+    Raw8<DT> r = zero_raw8<DT>();
+    if (n == 8 && width == 16) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            v[4 * i] = __uint_as_float(r.u[i].x);
-            v[4 * i + 1] = __uint_as_float(r.u[i].y);
-            v[4 * i + 2] = __uint_as_float(r.u[i].z);
-            v[4 * i + 3] = __uint_as_float(r.u[i].w);
+        for (int i = 0; i < W / 4; ++i) {
+            const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+            r.w[4 * i] = u.x, r.w[4 * i + 1] = u.y, r.w[4 * i + 2] = u.z, r.w[4 * i + 3] = u.w;
         }
+    } else if (n == 8 && width == 8) {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            const uint2 u = reinterpret_cast<const uint2*>(p)[i];
+            r.w[2 * i] = u.x, r.w[2 * i + 1] = u.y;
+        }
+    } else if (n == 8 && width == 4) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) r.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
     } else {
-        const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (DT == EP_BF16) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
+        for (int j = 0; j < 8; ++j)
+            if (j < n) {
+                if constexpr (DT == EP_F32) r.w[j] = reinterpret_cast<const uint32_t*>(p)[j];
+                else r.w[j / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(p)[j]) << (16 * (j % 2));
             }
-        }
+    }
+    return r;
+}
+
+// Elements 2i and 2i + 1 as floats.
+template <int DT>
+__device__ __forceinline__ float2 pair(const Raw8<DT>& r, int i) {
+    if constexpr (DT == EP_F32) return make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    else if constexpr (DT == EP_BF16) return make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
+}
+
+// The largest |v| as the bits of its own type without the sign, which are in the order of the values;
+// a NaN or an infinity is at least kInf.
+template <int DT>
+struct AbsBits {
+    static constexpr uint32_t kInf = DT == EP_F32 ? 0x7f800000u : DT == EP_BF16 ? 0x7f80u : 0x7c00u;
+};
+template <int DT>
+__device__ __forceinline__ uint32_t abs_max8(const Raw8<DT>& r) {
+    if constexpr (DT == EP_F32) {
+        uint32_t m = 0;
+#pragma unroll
+        for (uint32_t w : r.w) m = max(m, w & 0x7fffffffu);
+        return m;
+    } else {
+        uint32_t m = __vmaxu2(__vmaxu2(r.w[0] & 0x7fff7fffu, r.w[1] & 0x7fff7fffu),
+                              __vmaxu2(r.w[2] & 0x7fff7fffu, r.w[3] & 0x7fff7fffu));
+        return max(m & 0xffffu, m >> 16);
     }
 }
-
-// The first n (0 to 8) of eight elements, one by one; zeros behind them.
 template <int DT>
-__device__ __forceinline__ void load_some(const typename Elem<DT>::T* p, int n, float* v) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? to_float(p[j]) : 0.0f;
-}
-
-// max(a, |b|), NaN if either is.
-__device__ __forceinline__ float max_abs(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
-    return d;
-}
-__device__ __forceinline__ float abs_max8(const float* v) {
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max_abs(m, v[j]);
-    return m;
+__device__ __forceinline__ float abs_value(uint32_t bits) {
+    if constexpr (DT == EP_F32) return __uint_as_float(bits);
+    else if constexpr (DT == EP_BF16) return __uint_as_float(bits << 16);
+    else return __half2float(__ushort_as_half(uint16_t(bits)));
 }
 // The largest of `lanes` neighbouring lanes (a power of two), in each of them.
-__device__ __forceinline__ float lanes_max(float m, int lanes) {
-    for (int o = 1; o < lanes; o <<= 1) m = max_abs(m, __shfl_xor_sync(kFullMask, m, o));
+__device__ __forceinline__ uint32_t lanes_max(uint32_t m, int lanes) {
+    for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(kFullMask, m, o));
     return m;
 }
-__device__ __forceinline__ bool is_finite(float amax) { return amax < __int_as_float(0x7f800000); }
+
+// Two floats at a time.
+__device__ __forceinline__ unsigned long long as_u64(float2 v) {
+    return static_cast<unsigned long long>(__float_as_uint(v.x)) | (static_cast<unsigned long long>(__float_as_uint(v.y)) << 32);
+}
+__device__ __forceinline__ float2 as_float2(unsigned long long v) {
+    return make_float2(__uint_as_float(uint32_t(v)), __uint_as_float(uint32_t(v >> 32)));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_float2(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_float2(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+    return as_float2(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
 // floor(log2 x) of a normal x; at most -127 for smaller ones.
@@ -134,52 +178,84 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
     return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
 }
 
+// 1 / q, within one unit in the last place, and then (for a q of few bits) correctly rounded.
+__device__ __forceinline__ float reciprocal_near(float q) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(q));
+    return y;
+}
+__device__ __forceinline__ float reciprocal(float q) {
+    const float y = reciprocal_near(q);
+    return __fmaf_rn(y, __fmaf_rn(-q, y, 1.0f), y);
+}
+
 struct Block {
     uint32_t byte;  // the stored scale
-    float q, inv;   // element = E2M1(v / q); inv = 1 / q (0 where every element is 0)
+    float q, inv;   // element = E2M1(v / q); inv = 1 / q, 0 where every element is 0
+    float amax;
 };
-template <bool NV>
-__device__ __forceinline__ Block block_scale(float amax, float g, float g_inv) {
+// The scale of a block from the bits of its largest element.
+template <int DT, bool NV>
+__device__ __forceinline__ Block block_scale(uint32_t amax_bits, float g, float g_inv) {
     Block b;
+    b.amax = abs_value<DT>(amax_bits);
+    const bool fine = amax_bits < AbsBits<DT>::kInf;
     if constexpr (NV) {
-        b.byte = e4m3_of(__fdiv_rn(amax, 6.0f) * g_inv);
+        // amax / 6: for 16-bit elements the product with fl(1/6) is exact where it is on a border of
+        // two E4M3 values and far closer than the next element elsewhere; fp32 is corrected
+        constexpr float kSixth = 1.0f / 6.0f;
+        float t = b.amax * kSixth;
+        if constexpr (DT == EP_F32) t = __fmaf_rn(__fmaf_rn(-6.0f, t, b.amax), kSixth, t);
+        b.byte = e4m3_of(t * g_inv);
         b.q = e4m3x2_value(b.byte).x * g;
-        b.inv = b.q > 0.0f ? __frcp_rn(b.q) : 0.0f;
-        if (!is_finite(amax)) b.byte = 0x7f;
+        b.inv = !fine || b.q == 0.0f ? 0.0f : DT == EP_F32 ? reciprocal(b.q) : reciprocal_near(b.q);
+        if (!fine) b.byte = 0x7f;
     } else {
-        const int e = max(log2_floor(amax) - 2, -127);
-        b.byte = uint32_t(e + 127);
+        const int e = max(log2_floor(b.amax) - 2, -127);
+        b.byte = fine ? uint32_t(e + 127) : 255u;
         b.q = 1.0f;  // not used
-        b.inv = pow2f(-e);
-        if (!is_finite(amax)) b.byte = 255;
+        b.inv = fine ? pow2f(-e) : 0.0f;
     }
-    if (!is_finite(amax)) b.inv = 0.0f;
     return b;
 }
 
-__device__ __forceinline__ uint32_t e2m1_pack8(const float* x) {
+__device__ __forceinline__ uint32_t e2m1_pack8(const float2* x) {
     uint32_t r;
     asm("{\n .reg .b8 a, b, c, d;\n"
         " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
         " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
         " mov.b32 %0, {a, b, c, d};\n}"
         : "=r"(r)
-        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+        : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y));
     return r;
 }
 
 // Eight elements of one block as eight codes, the first in the lowest four bits.
 template <int DT, bool NV>
-__device__ __forceinline__ uint32_t quantize8(const float* v, const Block& b) {
-    if (b.inv == 0.0f) return 0;  // q = 0, or a NaN block
-    float x[8];
+__device__ __forceinline__ uint32_t quantize8(const Raw8<DT>& r, const Block& b) {
+    float2 x[4];
+    const float2 inv = both(b.inv);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        if constexpr (!NV) x[j] = v[j] * b.inv;
-        else if constexpr (DT == EP_F32) x[j] = __fdiv_rn(v[j], b.q);
-        else x[j] = __fadd_rn(__fmaf_rn(v[j], b.inv, 384.0f), -384.0f);
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = pair<DT>(r, i);
+        if constexpr (!NV) {
+            x[i] = mul2(v, inv);
+        } else if constexpr (DT != EP_F32) {
+            x[i] = add2(fma2(v, inv, both(384.0f)), both(-384.0f));
+        } else {
+            x[i] = mul2(v, inv);
+            x[i] = fma2(fma2(x[i], both(-b.q), v), inv, x[i]);
+        }
     }
-    return e2m1_pack8(x);
+    if constexpr (NV && DT == EP_F32)  // far above the block's range (a tensor scale given too small)
+        if (b.amax > 8.0f * b.q) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = pair<DT>(r, i);
+                x[i] = make_float2(__fdiv_rn(v.x, b.q), __fdiv_rn(v.y, b.q));
+            }
+        }
+    return b.inv == 0.0f ? 0u : e2m1_pack8(x);  // q = 0, or a NaN block
 }
 
 // The values of eight codes.
@@ -194,13 +270,6 @@ __device__ __forceinline__ void e2m1_values8(uint32_t codes, float* v) {
     }
 }
 
-// Eight floats to eight neighbouring elements, at once (16-byte aligned) or the first n one by one.
-template <int DT>
-__device__ __forceinline__ typename Elem<DT>::T from_float(float v) {
-    if constexpr (DT == EP_BF16) return __float2bfloat16_rn(v);
-    else if constexpr (DT == EP_FP16) return __float2half_rn(v);
-    else return v;
-}
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     uint32_t r;
@@ -208,21 +277,34 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
+// The first n of eight values to p, which is aligned to `width` bytes as for load_raw8.
 template <int DT>
-__device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float* v) {
-    if constexpr (DT == EP_F32) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
-                                                  pack2<DT>(v[6], v[7]));
-    }
-}
-template <int DT>
-__device__ __forceinline__ void store_some(typename Elem<DT>::T* p, int n, const float* v) {
+__device__ __forceinline__ void store8(typename Elem<DT>::T* p, int n, int width, const float* v) {
+    constexpr int W = DT == EP_F32 ? 8 : 4;
+    uint32_t w[W];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (j < n) p[j] = from_float<DT>(v[j]);
+    for (int i = 0; i < W; ++i) {
+        if constexpr (DT == EP_F32) w[i] = __float_as_uint(v[i]);
+        else w[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
+    }
+    if (n == 8 && width == 16) {
+#pragma unroll
+        for (int i = 0; i < W / 4; ++i)
+            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else if (n == 8 && width == 8) {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) reinterpret_cast<uint2*>(p)[i] = make_uint2(w[2 * i], w[2 * i + 1]);
+    } else if (n == 8 && width == 4) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) {
+                if constexpr (DT == EP_F32) reinterpret_cast<uint32_t*>(p)[j] = w[j];
+                else reinterpret_cast<uint16_t*>(p)[j] = uint16_t(w[j / 2] >> (16 * (j % 2)));
+            }
+    }
 }
 
 }  // namespace ms
@@ -236,6 +318,12 @@ inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline int64_t fp4_row_bytes(int64_t cols) { return 16 * div_up(cols, 32); }
 inline int64_t fp4_blocks(int format, int64_t cols) { return div_up(cols, format == EP_MXFP4 ? 32 : 16); }
 inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+// The widest access, 16, 8 or 4 bytes, that fits a pointer and strides (in bytes); else 1.
+inline int access_width(const void* p, int64_t stride, int64_t stride2 = 0) {
+    for (int w : {16, 8, 4})
+        if (aligned(p, size_t(w)) && stride % w == 0 && stride2 % w == 0) return w;
+    return 1;
+}
 
 // Launch as a programmatic dependent: the kernel may be set up while the one before it in the
 // stream still runs, and waits for it in wait_for_stream().

@@ -13,8 +13,8 @@ and every call is asynchronous on the current stream of that device (or on ``str
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -33,12 +33,28 @@ def _format(name: str, known: dict) -> int:
     return known[name]
 
 
+# The current stream's handle without a Stream object around it (3 us of a small call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+class _Here:
+    """Stands for a context that changes nothing."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *a):
+        pass
+
+
+_HERE = _Here()
+
+
 def _on(device: torch.device, stream):
     """(context in which `device` is current and temporaries belong to the call's stream, its handle)."""
+    index = device.index
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
-        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+        return (_HERE if index == torch.cuda.current_device() else torch.cuda.device(device)), _raw_stream(index)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream), stream.cuda_stream
@@ -50,27 +66,33 @@ def _cuda(t: torch.Tensor, what: str, device: torch.device | None = None) -> tor
     return t
 
 
+@functools.lru_cache(maxsize=4096)
+def _geometry(rows: int, cols: int, format: str):
+    """(C format, bytes of a row, scale tiles, where the tensor scale and the elements start, all bytes)."""
+    fmt = _format(format, FORMATS)
+    if not (0 <= rows < 2 ** 31 - 256 and 0 <= cols <= 2 ** 30):
+        raise ValueError("FP4Tensor: size out of range")
+    row_bytes = 16 * (-(-cols // 32))
+    tiles = (-(-rows // 128), -(-(-(-cols // BLOCK[format])) // 4))
+    n = 512 * tiles[0] * tiles[1]
+    return fmt, row_bytes, tiles, (n, n + 4 * SCALE_FLOATS), n + 4 * SCALE_FLOATS + rows * row_bytes
+
+
 class FP4Tensor:
     """A rows x cols matrix in microscaled 4-bit floating point: ``data`` (uint8, rows x row bytes),
     ``scales`` (uint8, the tiled layout) and ``tensor_scale`` (one float32), views of one buffer."""
 
+    __slots__ = ("format", "shape", "device", "view", "_ref", "_buffer", "_row_bytes", "_scale_tiles", "_at")
+
     def __init__(self, shape, format: str, device=None):
-        self.format, self.shape = format, (int(shape[0]), int(shape[1]))
-        self._fmt = _format(format, FORMATS)
-        rows, cols = self.shape
-        if not (0 <= rows < 2 ** 31 - 256 and 0 <= cols <= 2 ** 30):
-            raise ValueError("FP4Tensor: size out of range")
-        self._row_bytes = 16 * (-(-cols // 32))
-        blocks = -(-cols // BLOCK[format])
-        self._scale_tiles = (-(-rows // 128), -(-blocks // 4))
-        n = 512 * self._scale_tiles[0] * self._scale_tiles[1]
-        # the scales first (whole 512-byte tiles), the tensor scale and its work space, the elements
-        self._at = (n, n + 4 * SCALE_FLOATS)
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        self._buffer = torch.empty(self._at[1] + rows * self._row_bytes, dtype=torch.uint8, device=dev)
-        self.device = self._buffer.device
-        p = self._buffer.data_ptr()
-        self.view = EpFP4Tensor(p + self._at[1], p, p + n, self.device.index, self._fmt, rows, cols)
+        rows, cols = shape
+        # the scales first (whole 512-byte tiles), then the tensor scale and its work space, the elements
+        fmt, self._row_bytes, self._scale_tiles, self._at, size = _geometry(rows, cols, format)
+        self.format, self.shape = format, (rows, cols)
+        self._buffer = buffer = torch.empty(size, dtype=torch.uint8, device="cuda" if device is None else device)
+        self.device = buffer.device
+        p = buffer.data_ptr()
+        self.view = EpFP4Tensor(p + self._at[1], p, p + self._at[0], self.device.index, fmt, rows, cols)
         self._ref = ctypes.byref(self.view)
 
     @property
@@ -83,7 +105,7 @@ class FP4Tensor:
 
     @property
     def tensor_scale(self) -> torch.Tensor:
-        return self._buffer[self._at[0]:self._at[0] + 4].view(torch.float32)
+        return self._buffer.narrow(0, self._at[0], 4).view(torch.float32)
 
     @property
     def nbytes(self) -> int:
