@@ -15,8 +15,8 @@ using namespace ms;
 constexpr int kThreads = 256;
 constexpr int kMaxHeadDim = 1024;
 constexpr int kLaunchTokens = 4096;  // tokens of one write launch
-constexpr int kMaxWriteTokens = 8;   // tokens of one block of a write
-constexpr int kReadTokens = 16;      // tokens of one block of a read
+constexpr int kMaxWriteTokens = 8;   // most tokens of one block of a write
+constexpr int kMaxReadTokens = 64;   // most tokens of one block of a read
 constexpr int kSharedSeqs = 1024;    // sequence starts that a read searches in shared memory
 
 struct CacheView {
@@ -27,7 +27,6 @@ struct CacheView {
     void* heads;          // source or output rows
     int64_t token_stride, head_stride;
     int head_dim;
-    int lanes;            // lanes of one row: a power of two, 8 elements each (4 x 8 above 256)
     int width;            // alignment of its rows for load_raw8 and store8
 };
 
@@ -46,8 +45,10 @@ struct ReadArgs {
     const int32_t* page_table;
     int64_t table_stride, pages_per_seq, n_pages, tokens;
     const int32_t* cu_seqlens;
-    int n_seqs, page_size, heads;
+    int n_seqs, page_size;
+    int n, heads;         // caches, and heads of each
     float heads_inv;
+    int per_block;        // tokens of one block
 };
 
 // r / d for 0 <= r <= 2^20 and d_inv = 1.0f / d: (r + 1/2) / d is at least 1 / (2 d) away from an integer,
@@ -119,16 +120,14 @@ __device__ __forceinline__ uint2 e4m3_payload(const Raw8<DT>& v, float inv) {
 }
 
 // The payload (and by its first lane the scale) of one row, of which this lane holds chunks of 8
-// elements `lane`, `lane + lanes`, ...; they are zeros past the row's end.
-template <int DT, int FMT, int NC>
-__device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int lane, const Raw8<DT>* v, bool live) {
-    uint8_t* data = c.data + row * c.row_bytes;
-    uint8_t* scales = c.scales + row * c.scale_bytes;
+// elements `lane`, `lane + LANES`, ...; they are zeros past the row's end.
+template <int DT, int FMT, int LANES, int NC>
+__device__ __forceinline__ void write_row(const CacheView& c, uint8_t* data, uint8_t* scales, int lane, const Raw8<DT>* v, bool live) {
     if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
         uint32_t bits = 0;
 #pragma unroll
         for (int k = 0; k < NC; ++k) bits = max(bits, abs_max8<DT>(v[k]));
-        bits = lanes_max(bits, c.lanes);
+        bits = lanes_max<LANES>(bits);
         const bool fine = bits < AbsBits<DT>::kInf;
         const float amax = abs_value<DT>(bits);
         float s, inv;
@@ -145,7 +144,7 @@ __device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int l
         if (lane == 0) *reinterpret_cast<float*>(scales) = s;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            const int at = 8 * (lane + k * c.lanes);
+            const int at = 8 * (lane + k * LANES);
             if (at >= c.head_dim) break;
             uint2 w = make_uint2(0, 0);
             if (fine && inv > 0.0f) {
@@ -164,24 +163,26 @@ __device__ __forceinline__ void write_row(const CacheView& c, int64_t row, int l
         constexpr bool NV = FMT == EP_NVFP4;
 #pragma unroll
         for (int k = 0; k < NC; ++k) {
-            const int chunk = lane + k * c.lanes, at = 8 * chunk;
-            const Block b = block_scale<DT, NV>(lanes_max(abs_max8<DT>(v[k]), NV ? 2 : 4), 1.0f, 1.0f);
+            const int chunk = lane + k * LANES, at = 8 * chunk;
+            const Block b = block_scale<DT, NV>(lanes_max<NV ? 2 : 4>(abs_max8<DT>(v[k])), 1.0f, 1.0f);
             const uint32_t codes = quantize8<DT, NV>(v[k], b);
-            if (!live || at / 2 >= c.row_bytes) continue;
+            if (!live || at / 2 >= int(c.row_bytes)) continue;
             *reinterpret_cast<uint32_t*>(data + at / 2) = codes;
             if (chunk % (NV ? 2 : 4) == 0 && at < c.head_dim) scales[chunk / (NV ? 2 : 4)] = uint8_t(b.byte);
         }
     }
 }
 
-// A block takes a few tokens, all heads of every cache.  First it looks through the later tokens of the
-// launch for its own slots: a token whose slot is named again later is dropped, so that payload and
-// scale of a slot always come from one token (launches of one call follow each other, the later wins).
-// Rows then go in batches, whose loads are all on their way before the first is used.
-template <int DT, int FMT, int NC>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteArgs a) {
+// A block takes a few tokens, all heads, of every cache (or of one, blockIdx.y, where there are few
+// tokens).  First it looks through the later tokens of the launch for its own slots: a token whose slot
+// is named again later is dropped, so that payload and scale of a slot always come from one token
+// (launches of one call follow each other, the later wins).  Rows then go in batches of LANES lanes a
+// row, whose loads are all on their way before the first is used.
+template <int DT, int FMT, int LANES, int NC>
+__global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) cache_write_kernel(const __grid_constant__ WriteArgs a) {
     using T = typename Elem<DT>::T;
-    constexpr int kBatch = NC == 1 ? (DT == EP_F32 ? 2 : 4) : 1;
+    constexpr int kBatch = NC == 1 && DT != EP_F32 ? 4 : NC == 1 ? 2 : 1;
+    constexpr int kStep = kThreads / LANES;
     __shared__ int64_t slot[kMaxWriteTokens];
     __shared__ int dropped[kMaxWriteTokens];
     wait_for_stream();
@@ -197,37 +198,46 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     for (int i = 0; i < n; ++i)
         if (slot[i] >= 0) lo = min(lo, slot[i]), hi = max(hi, slot[i]);
     if (hi >= 0)
-        for (int64_t j = t0 + 1 + threadIdx.x; j < a.tokens; j += kThreads) {
-            const int64_t s = a.slots[j];
-            if (s < lo || s > hi) continue;
-            for (int i = 0; i < n; ++i)
-                if (slot[i] == s && t0 + i < j) dropped[i] = 1;
+        for (int64_t j0 = t0 + 1 + threadIdx.x; j0 < a.tokens; j0 += 4 * kThreads) {
+            int64_t s[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s[u] = j0 + u * kThreads < a.tokens ? a.slots[j0 + u * kThreads] : -1;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (s[u] >= lo && s[u] <= hi)
+                    for (int i = 0; i < n; ++i)
+                        if (slot[i] == s[u] && t0 + i < j0 + u * kThreads) dropped[i] = 1;
         }
     __syncthreads();
+    if (int(threadIdx.x) < n && dropped[threadIdx.x]) slot[threadIdx.x] = -1;
+    __syncthreads();
 
-    const int rows = n * a.heads;
-    for (int ci = 0; ci < a.n; ++ci) {
+    const int rows = n * a.heads, lane = threadIdx.x % LANES;
+    for (int ci = blockIdx.y; ci < a.n; ci += gridDim.y) {
         const CacheView& c = a.c[ci];
-        const int lane = threadIdx.x % c.lanes, step = kThreads / c.lanes;
+        const T* src = static_cast<const T*>(c.heads) + t0 * c.token_stride;
         // every lane of a warp stays in the loop: rows past the end are zeros and not written
-        for (int base = int(threadIdx.x) / c.lanes; base - int(threadIdx.x) / c.lanes < rows; base += kBatch * step) {
+        for (int base = 0; base < rows; base += kBatch * kStep) {
             Raw8<DT> v[kBatch][NC];
-            int64_t at[kBatch];
+            int64_t row[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                const int r = base + u * step;
+                const int r = base + u * kStep + int(threadIdx.x) / LANES;
                 const int i = min(quotient(r, a.heads_inv), n - 1), h = r - i * a.heads;
-                const bool live = r < rows && slot[i] >= 0 && !dropped[i];
-                at[u] = live ? slot[i] * a.heads + h : -1;
-                const T* src = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride;
+                row[u] = r < rows && slot[i] >= 0 ? slot[i] * a.heads + h : -1;
+                const T* p = src + i * c.token_stride + h * c.head_stride;
 #pragma unroll
                 for (int k = 0; k < NC; ++k) {
-                    const int e = 8 * (lane + k * c.lanes);
-                    v[u][k] = load_raw8<DT>(src + e, live ? max(0, min(8, c.head_dim - e)) : 0, c.width);
+                    const int e = 8 * (lane + k * LANES);
+                    v[u][k] = load_raw8<DT>(p + e, row[u] >= 0 ? min(8, c.head_dim - e) : 0, c.width);
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) write_row<DT, FMT, NC>(c, max(at[u], int64_t(0)), lane, v[u], at[u] >= 0);
+            for (int u = 0; u < kBatch; ++u) {
+                if (base + u * kStep >= rows) break;
+                write_row<DT, FMT, LANES, NC>(c, c.data + row[u] * c.row_bytes, c.scales + row[u] * c.scale_bytes, lane, v[u],
+                                              row[u] >= 0);
+            }
         }
     }
 }
@@ -295,17 +305,18 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seqs, int64_
     return lo;
 }
 
-// A block takes 16 tokens of one output, all heads: finds their slots, then reads rows in batches,
-// whose loads are all on their way before the first is used.
-template <int DT, int FMT>
+// A block takes up to 64 tokens, all heads, of every output (or of one, blockIdx.y, where there are few
+// tokens): finds their slots, then reads rows of LANES lanes in batches, whose loads are all on their way
+// before the first is used.
+template <int DT, int FMT, int LANES>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
     using T = typename Elem<DT>::T;
+    constexpr int kBatch = 4, kStep = kThreads / LANES;
     __shared__ int32_t starts[kSharedSeqs + 1];
-    __shared__ int64_t slot[kReadTokens];  // -1: zeros, -2: past the sequences
+    __shared__ int64_t slot[kMaxReadTokens];  // -1: zeros, -2: past the sequences
     wait_for_stream();
-    const CacheView& c = a.c[blockIdx.y];
-    const int64_t t0 = int64_t(blockIdx.x) * kReadTokens;
-    const int n = int(min(int64_t(kReadTokens), a.tokens - t0));
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
+    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
     const bool shared = a.n_seqs <= kSharedSeqs;
     if (shared)
         for (int i = threadIdx.x; i <= a.n_seqs; i += kThreads) starts[i] = a.cu_seqlens[i];
@@ -316,67 +327,80 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
         int64_t s = -2;
         const int seq = sequence_of(cu, a.n_seqs, t);
         const int64_t pos = t - cu[seq];
-        if (pos >= 0 && t < cu[seq + 1]) {
+        if (pos >= 0 && t < cu[seq + 1]) {  // both differences fit 32 bits: tokens do
             s = -1;
-            const int64_t p = pos / a.page_size;
-            if (p < a.pages_per_seq) {
+            const uint32_t p = uint32_t(pos) / uint32_t(a.page_size);
+            if (int64_t(p) < a.pages_per_seq) {
                 const int64_t page = a.page_table[seq * a.table_stride + p];
-                if (page >= 0 && page < a.n_pages) s = page * a.page_size + pos % a.page_size;
+                if (page >= 0 && page < a.n_pages) s = page * a.page_size + (uint32_t(pos) - p * uint32_t(a.page_size));
             }
         }
         slot[threadIdx.x] = s;
     }
     __syncthreads();
-    constexpr int kBatch = 4;
-    const int chunks = (c.head_dim + 7) / 8, rows = n * a.heads, step = kThreads / c.lanes;
-    for (int chunk = threadIdx.x % c.lanes; chunk < chunks; chunk += c.lanes)
-        for (int base = int(threadIdx.x) / c.lanes; base < rows; base += kBatch * step) {
-            Chunk<FMT> q[kBatch];
-            int64_t at[kBatch];
+    const int rows = n * a.heads;
+    for (int ci = blockIdx.y; ci < a.n; ci += gridDim.y) {
+        const CacheView& c = a.c[ci];
+        T* out = static_cast<T*>(c.heads) + t0 * c.token_stride;
+        const int chunks = (c.head_dim + 7) / 8;
+        for (int chunk = threadIdx.x % LANES; chunk < chunks; chunk += LANES)
+            for (int base = int(threadIdx.x) / LANES; base < rows; base += kBatch * kStep) {
+                Chunk<FMT> q[kBatch];
+                T* dst[kBatch];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int r = min(base + u * step, rows - 1);
-                const int t = quotient(r, a.heads_inv), h = r - t * a.heads;
-                at[u] = base + u * step < rows && slot[t] != -2 ? (t0 + t) * c.token_stride + h * c.head_stride + 8 * chunk : -1;
-                q[u] = load_chunk<FMT>(c, slot[t] < 0 ? -1 : slot[t] * a.heads + h, chunk);
-            }
+                for (int u = 0; u < kBatch; ++u) {
+                    const int r = base + u * kStep;
+                    const int t = min(quotient(r, a.heads_inv), n - 1), h = r - t * a.heads;
+                    const int64_t s = slot[t];
+                    dst[u] = r < rows && s != -2 ? out + t * c.token_stride + h * c.head_stride + 8 * chunk : nullptr;
+                    q[u] = load_chunk<FMT>(c, r < rows && s >= 0 ? s * a.heads + h : -1, chunk);
+                }
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                if (at[u] < 0) continue;
-                float v[8];
-                chunk_values<FMT>(q[u], v);
-                store8<DT>(static_cast<T*>(c.heads) + at[u], min(8, c.head_dim - 8 * chunk), c.width, v);
+                for (int u = 0; u < kBatch; ++u) {
+                    if (!dst[u]) continue;
+                    float v[8];
+                    chunk_values<FMT>(q[u], v);
+                    store8<DT>(dst[u], min(8, c.head_dim - 8 * chunk), c.width, v);
+                }
             }
-        }
+    }
 }
 
 // ---- host side -----------------------------------------------------------------------------------
+// Lanes of a row: a power of two of at least 4 (a block of 32 elements), 8 elements each.
+int lanes_of(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
+
 template <int DT, int FMT>
-cudaError_t launch_write(const WriteArgs& w, bool wide, cudaStream_t st) {
-    const dim3 grid(unsigned(op::div_up(w.tokens, w.per_block)));
-    return op::launch(wide ? cache_write_kernel<DT, FMT, 4> : cache_write_kernel<DT, FMT, 1>, grid, dim3(kThreads), 0, st, w);
+cudaError_t launch_write(const WriteArgs& w, int head_dim, dim3 grid, cudaStream_t st) {
+    const auto kernel = head_dim > 256            ? cache_write_kernel<DT, FMT, 32, 4>
+                        : lanes_of(head_dim) == 32 ? cache_write_kernel<DT, FMT, 32, 1>
+                        : lanes_of(head_dim) == 16 ? cache_write_kernel<DT, FMT, 16, 1>
+                                                   : cache_write_kernel<DT, FMT, 8, 1>;
+    return op::launch(kernel, grid, dim3(kThreads), 0, st, w);
 }
 template <int DT>
-cudaError_t write_as(int fmt, const WriteArgs& w, bool wide, cudaStream_t st) {
+cudaError_t write_as(int fmt, const WriteArgs& w, int head_dim, dim3 grid, cudaStream_t st) {
     switch (fmt) {
-        case EP_FP8_E4M3: return launch_write<DT, EP_FP8_E4M3>(w, wide, st);
-        case EP_INT8: return launch_write<DT, EP_INT8>(w, wide, st);
-        case EP_MXFP4: return launch_write<DT, EP_MXFP4>(w, wide, st);
-        default: return launch_write<DT, EP_NVFP4>(w, wide, st);
+        case EP_FP8_E4M3: return launch_write<DT, EP_FP8_E4M3>(w, head_dim, grid, st);
+        case EP_INT8: return launch_write<DT, EP_INT8>(w, head_dim, grid, st);
+        case EP_MXFP4: return launch_write<DT, EP_MXFP4>(w, head_dim, grid, st);
+        default: return launch_write<DT, EP_NVFP4>(w, head_dim, grid, st);
     }
 }
 template <int DT, int FMT>
-cudaError_t launch_read(const ReadArgs& r, int n, cudaStream_t st) {
-    const dim3 grid(unsigned(op::div_up(r.tokens, kReadTokens)), unsigned(n));
-    return op::launch(cache_read_kernel<DT, FMT>, grid, dim3(kThreads), 0, st, r);
+cudaError_t launch_read(const ReadArgs& r, int head_dim, dim3 grid, cudaStream_t st) {
+    const auto kernel = lanes_of(head_dim) == 32   ? cache_read_kernel<DT, FMT, 32>
+                        : lanes_of(head_dim) == 16 ? cache_read_kernel<DT, FMT, 16>
+                                                   : cache_read_kernel<DT, FMT, 8>;
+    return op::launch(kernel, grid, dim3(kThreads), 0, st, r);
 }
 template <int DT>
-cudaError_t read_as(int fmt, const ReadArgs& r, int n, cudaStream_t st) {
+cudaError_t read_as(int fmt, const ReadArgs& r, int head_dim, dim3 grid, cudaStream_t st) {
     switch (fmt) {
-        case EP_FP8_E4M3: return launch_read<DT, EP_FP8_E4M3>(r, n, st);
-        case EP_INT8: return launch_read<DT, EP_INT8>(r, n, st);
-        case EP_MXFP4: return launch_read<DT, EP_MXFP4>(r, n, st);
-        default: return launch_read<DT, EP_NVFP4>(r, n, st);
+        case EP_FP8_E4M3: return launch_read<DT, EP_FP8_E4M3>(r, head_dim, grid, st);
+        case EP_INT8: return launch_read<DT, EP_INT8>(r, head_dim, grid, st);
+        case EP_MXFP4: return launch_read<DT, EP_MXFP4>(r, head_dim, grid, st);
+        default: return launch_read<DT, EP_NVFP4>(r, head_dim, grid, st);
     }
 }
 
@@ -390,7 +414,7 @@ int make_views(const ep_cache* caches, const ep_heads* h, int n, const char* who
         if (!fp4 && c.format != EP_FP8_E4M3 && c.format != EP_INT8) return set_error(EP_ERR_DTYPE, w + ": unsupported cache format");
         const int es = op::elem_bytes(x.dtype);
         if (es == 0) return set_error(EP_ERR_DTYPE, w + ": heads must be EP_BF16, EP_FP16 or EP_F32");
-        if (c.n_pages < 0 || c.page_size < 1 || c.heads < 1 || c.head_dim < 1 || c.head_dim > kMaxHeadDim || c.heads > 65536 ||
+        if (c.n_pages < 0 || c.page_size < 1 || c.heads < 1 || c.head_dim < 1 || c.head_dim > kMaxHeadDim || c.heads > 4096 ||
             c.n_pages > (int64_t(1) << 40) / c.page_size)
             return set_error(EP_ERR_SHAPE, w + ": cache geometry out of range");
         if (x.tokens < 0 || x.tokens > 0x7fffffff || x.heads != c.heads || x.head_dim != c.head_dim)
@@ -413,8 +437,6 @@ int make_views(const ep_cache* caches, const ep_heads* h, int n, const char* who
         v.token_stride = x.token_stride;
         v.head_stride = x.head_stride;
         v.head_dim = c.head_dim;
-        v.lanes = 4;  // a 4-bit block is 2 or 4 lanes
-        while (v.lanes < 32 && 8 * v.lanes < c.head_dim) v.lanes *= 2;
         v.width = op::access_width(x.data, x.token_stride * es, x.head_stride * es);
     }
     return EP_OK;
@@ -447,7 +469,7 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
     if (tokens > 0 && (!slots || !op::aligned(slots, 8))) return set_error(EP_ERR_ARG, "ep_cache_write: slots are NULL or misaligned");
     rc = device_of(caches, src, n, "ep_cache_write", sms);
     if (rc != EP_OK || tokens == 0 || caches[0].n_pages == 0) return rc;
-    const bool wide = src[0].head_dim > 256 || (n == 2 && src[1].head_dim > 256);
+    const int dim = std::max(src[0].head_dim, src[n - 1].head_dim);
     const int es = op::elem_bytes(src[0].dtype);
     w.n_slots = caches[0].n_pages * caches[0].page_size;
     w.n = n;
@@ -460,11 +482,12 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
         part.tokens = std::min<int64_t>(kLaunchTokens, tokens - t0);
         for (int i = 0; i < n; ++i)
             part.c[i].heads = static_cast<uint8_t*>(w.c[i].heads) + t0 * w.c[i].token_stride * es;
-        // few tokens are spread over as many blocks as there are SMs
+        // few tokens are spread over the SMs, keys and values apart
         part.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxWriteTokens, part.tokens / (2 * sms))));
-        const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, wide, st)
-                              : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, wide, st)
-                                                        : write_as<EP_F32>(caches[0].format, part, wide, st);
+        const dim3 grid(unsigned(op::div_up(part.tokens, part.per_block)), part.per_block < kMaxWriteTokens ? unsigned(n) : 1u);
+        const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, dim, grid, st)
+                              : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, dim, grid, st)
+                                                        : write_as<EP_F32>(caches[0].format, part, dim, grid, st);
         if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_cache_write: ") + cudaGetErrorString(e));
     }
     return EP_OK;
@@ -494,10 +517,15 @@ extern "C" int ep_cache_read(const ep_cache* caches, const ep_heads* out, int n,
     r.page_size = caches[0].page_size;
     r.heads = caches[0].heads;
     r.heads_inv = 1.0f / float(r.heads);
+    r.n = n;
+    // few tokens are spread over the SMs, keys and values apart
+    r.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxReadTokens, r.tokens / (4 * sms))));
+    const dim3 grid(unsigned(op::div_up(r.tokens, r.per_block)), r.per_block < kMaxReadTokens ? unsigned(n) : 1u);
+    const int dim = std::max(out[0].head_dim, out[n - 1].head_dim);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = out[0].dtype == EP_BF16   ? read_as<EP_BF16>(caches[0].format, r, n, st)
-                          : out[0].dtype == EP_FP16 ? read_as<EP_FP16>(caches[0].format, r, n, st)
-                                                    : read_as<EP_F32>(caches[0].format, r, n, st);
+    const cudaError_t e = out[0].dtype == EP_BF16   ? read_as<EP_BF16>(caches[0].format, r, dim, grid, st)
+                          : out[0].dtype == EP_FP16 ? read_as<EP_FP16>(caches[0].format, r, dim, grid, st)
+                                                    : read_as<EP_F32>(caches[0].format, r, dim, grid, st);
     if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_cache_read: ") + cudaGetErrorString(e));
     return EP_OK;
 }

@@ -54,10 +54,10 @@ __device__ __forceinline__ uint32_t finite_max8(const Raw8<DT>& r) {
 
 // The largest of a block's threads, in all of them.
 __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* smem) {
-    m = lanes_max(m, 32);
+    m = lanes_max<32>(m);
     if (threadIdx.x % 32 == 0) smem[threadIdx.x / 32] = m;
     __syncthreads();
-    return lanes_max(smem[threadIdx.x % (kThreads / 32)], kThreads / 32);
+    return lanes_max<kThreads / 32>(smem[threadIdx.x % (kThreads / 32)]);
 }
 
 // Chunks of eight elements `first`, `first + step`, ... of x, row by row; four in flight.
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 3) quantize_kernel(const QuantArgs a
 #pragma unroll
         for (int p = 0; p < kBatch; ++p) {
             const int r = sub + (p0 + p) * kPassRows;
-            const Block b = block_scale<DT, NV>(lanes_max(abs_max8<DT>(v[p]), NV ? 2 : 4), g, g_inv);
+            const Block b = block_scale<DT, NV>(lanes_max<NV ? 2 : 4>(abs_max8<DT>(v[p])), g, g_inv);
             const uint32_t codes = quantize8<DT, NV>(v[p], b);
             const bool in = r < rows;
             if (in && codes_in) *reinterpret_cast<uint32_t*>(data + int64_t(p0 + p) * kPassRows * a.row_bytes) = codes;

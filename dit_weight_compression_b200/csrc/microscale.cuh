@@ -59,6 +59,7 @@ template <int DT>
 __device__ __forceinline__ Raw8<DT> load_raw8(const typename Elem<DT>::T* p, int n, int width) {
     constexpr int W = DT == EP_F32 ? 8 : 4;
     Raw8<DT> r = zero_raw8<DT>();
+    if (n <= 0) return r;
     if (n == 8 && width == 16) {
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
@@ -118,9 +119,11 @@ __device__ __forceinline__ float abs_value(uint32_t bits) {
     else if constexpr (DT == EP_BF16) return __uint_as_float(bits << 16);
     else return __half2float(__ushort_as_half(uint16_t(bits)));
 }
-// The largest of `lanes` neighbouring lanes (a power of two), in each of them.
-__device__ __forceinline__ uint32_t lanes_max(uint32_t m, int lanes) {
-    for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(kFullMask, m, o));
+// The largest of LANES neighbouring lanes (a power of two), in each of them.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) m = max(m, __shfl_xor_sync(kFullMask, m, o));
     return m;
 }
 

@@ -297,7 +297,7 @@ typedef struct {
     int format;      /* EP_FP8_E4M3, EP_INT8, EP_MXFP4 or EP_NVFP4                                */
     int64_t n_pages;
     int page_size;
-    int heads;
+    int heads;       /* 1 to 4096                                                                 */
     int head_dim;    /* 1 to 1024                                                                 */
 } ep_cache;
 
