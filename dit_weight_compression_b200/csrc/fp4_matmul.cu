@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) fp4_matmul_kernel(const __grid_const
     auto full = [&](int s) { return bars + 8 * s; };
     auto empty = [&](int s) { return bars + 8 * (G::kStages + s); };
     const uint32_t done = bars + 16 * G::kStages, slot = done + 8;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = int(uniform(threadIdx.x / 32)), lane = threadIdx.x % 32;
     uint32_t ranks, rank = cluster_rank();
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
     const int tile = int(blockIdx.x / ranks);
@@ -134,61 +134,66 @@ __global__ void __launch_bounds__(kThreads) fp4_matmul_kernel(const __grid_const
     fence_after();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+    tmem = uniform(tmem);
     ms::wait_for_stream();
 
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) {
-            const bool second = G::kQBlocks == 2 && q0 + 128 < a.q_rows;
-            int issued = 0;
-            for (int it = 0; it < steps && ok; ++it) {
-                const int s = it % G::kStages, k = k0 + it;
-                if (it >= G::kStages) ok = bar_wait(empty(s), (it / G::kStages - 1) & 1);
-                if (!ok) break;
-                const int tiles = min(G::kScaleTiles, a.scale_tiles - k * G::kScaleTiles);
-                const uint32_t st = base + s * G::kStage;
+        const bool leader = elect_one(), second = G::kQBlocks == 2 && q0 + 128 < a.q_rows;
+        int issued = 0;
+        for (int it = 0; it < steps; ++it) {
+            const int s = it % G::kStages, k = k0 + it;
+            if (it >= G::kStages && !(ok = bar_wait(empty(s), (it / G::kStages - 1) & 1))) break;
+            const int tiles = min(G::kScaleTiles, a.scale_tiles - k * G::kScaleTiles);
+            const uint32_t st = base + s * G::kStage;
+            const int64_t at = int64_t(k) * G::kScaleTiles;
+            if (leader) {
                 bar_expect(full(s), G::kP + G::kQ + 512 * tiles * (second ? 3 : 2));
                 tma_2d(st, &p_map, 128 * k, p0, full(s));
                 tma_2d(st + G::kP, &q_map, 128 * k, q0, full(s));
-                const int64_t at = int64_t(k) * G::kScaleTiles;
                 bulk_copy(st + G::kP + G::kQ, a.p_scales + (int64_t(p0 / 128) * a.scale_tiles + at) * 512, 512 * tiles, full(s));
-                for (int b = 0; b < (second ? 2 : 1); ++b)
-                    bulk_copy(st + G::kP + G::kQ + G::kPS * (1 + b),
-                              a.q_scales + ((int64_t(q0) / 128 + b) * a.scale_tiles + at) * 512, 512 * tiles, full(s));
-                issued = it + 1;
-            }
-            // nothing may still be on its way into this CTA's memory when it leaves
-            for (int it = max(0, issued - G::kStages); it < issued; ++it) ok &= bar_wait(full(it % G::kStages), (it / G::kStages) & 1);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
-            for (int it = 0; it < steps; ++it) {
-                const int s = it % G::kStages;
-                ok = bar_wait(full(s), (it / G::kStages) & 1);
-                if (!ok) break;
-                fence_after();
-                const uint32_t st = base + s * G::kStage;
-                const uint32_t sp = tmem + G::kSum + s * G::kScaleCols, sq = sp + 4 * G::kScaleTiles;
-                const int products = min(4, a.k64 - 4 * (k0 + it)), tiles = NV ? products : (products + 1) / 2;
-                for (int t = 0; t < tiles; ++t) {
-                    copy_scales(sp + 4 * t, scale_desc(st + G::kP + G::kQ + 512 * t));
 #pragma unroll
-                    for (int b = 0; b < G::kQBlocks; ++b)
-                        copy_scales(sq + 4 * (t * G::kQBlocks + b), scale_desc(st + G::kP + G::kQ + G::kPS * (1 + b) + 512 * t));
-                }
-                const uint64_t da = operand_desc(st), db = operand_desc(st + G::kP);
-                for (int j = 0; j < products; ++j) {
-                    const int t = NV ? j : j / 2;
-                    mma_fp4<NV>(tmem, da + 2 * j, db + 2 * j, mma_fp4_idesc<NV>(NT, j % 2), sp + 4 * t, sq + 4 * G::kQBlocks * t,
-                                it > 0 || j > 0);
-                }
+                for (int b = 0; b < G::kQBlocks; ++b)
+                    if (b == 0 || second)
+                        bulk_copy(st + G::kP + G::kQ + G::kPS * (1 + b),
+                                  a.q_scales + ((int64_t(q0) / 128 + b) * a.scale_tiles + at) * 512, 512 * tiles, full(s));
+            }
+            issued = it + 1;
+        }
+        // nothing may still be on its way into this CTA's memory when it leaves
+        for (int it = max(0, issued - G::kStages); it < issued; ++it) ok &= bar_wait(full(it % G::kStages), (it / G::kStages) & 1);
+    } else if (warp == 1) {
+        const bool leader = elect_one();
+        for (int it = 0; it < steps; ++it) {
+            const int s = it % G::kStages;
+            if (!(ok = bar_wait(full(s), (it / G::kStages) & 1))) break;
+            fence_after();
+            const uint32_t st = base + s * G::kStage;
+            const uint32_t sp = tmem + G::kSum + s * G::kScaleCols, sq = sp + 4 * G::kScaleTiles;
+            const uint32_t da = operand_low(st), db = operand_low(st + G::kP), ds = scale_low(st + G::kP + G::kQ);
+            const int products = min(4, a.k64 - 4 * (k0 + it)), tiles = NV ? products : (products + 1) / 2;
+            if (leader) {
+#pragma unroll
+                for (int t = 0; t < G::kScaleTiles; ++t)
+                    if (t < tiles) {
+                        copy_scales(sp + 4 * t, desc(ds + 32 * t, kScaleHigh));
+#pragma unroll
+                        for (int b = 0; b < G::kQBlocks; ++b)
+                            copy_scales(sq + 4 * (t * G::kQBlocks + b), desc(ds + (G::kPS * (1 + b) >> 4) + 32 * t, kScaleHigh));
+                    }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < products) {
+                        const int t = NV ? j : j / 2;
+                        mma_fp4<NV>(tmem, desc(da + 2 * j, kOperandHigh), desc(db + 2 * j, kOperandHigh), mma_fp4_idesc<NV>(NT, j % 2),
+                                    sp + 4 * t, sq + 4 * G::kQBlocks * t, it > 0 || j > 0);
+                    }
                 commit(empty(s));
             }
-            commit(done);
         }
-        __syncwarp();
+        if (leader) commit(done);
     }
+    __syncwarp();
     // every warp: the sums are ready, and no copy or product uses the stages any more
     ok &= bar_wait(done, 0);
     fence_after();
@@ -273,6 +278,180 @@ __global__ void __launch_bounds__(kThreads) fp4_matmul_kernel(const __grid_const
     if (warp == 2) tmem_free(tmem, G::kColumns);
 }
 
+// ---- long products ---------------------------------------------------------------------------------
+// Persistent pairs of CTAs, each pair on tiles of 256 x 256: a CTA holds 128 rows of a (the tensor core's
+// lanes) and half of the tile's rows of b, so that of every operand byte brought to an SM twice as much is
+// used as by a CTA alone.  Warp 0 copies, warp 1 of the first CTA issues products for both, warps 2 to 9
+// take the sums: they read all of them into registers, give the accumulator back, and write while the next
+// tile's products run.  (Tensor memory: 256 columns of sums leave 256 for scales, so the accumulator is
+// single; reading it takes a few hundred of a tile's 64 cycles per 32 columns of K.)
+template <bool NV>
+struct PairGeo {
+    static constexpr int kScaleTiles = NV ? 4 : 2;
+    static constexpr int kOperand = 128 * 128;                 // a's rows, and as much of b
+    static constexpr int kAS = kScaleTiles * 512, kBS = 2 * kScaleTiles * 512;
+    static constexpr int kStage = 2 * kOperand + kAS + kBS;
+    static constexpr int kStages = 5;
+    static constexpr int kScaleCols = 4 * kScaleTiles * 3;
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 256;
+    static constexpr int kThreads = 320;
+    static_assert(256 + kStages * kScaleCols <= 512, "tensor memory");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct PairArgs {
+    MatmulArgs m;
+    int a_tiles, b_tiles;     // tiles of 256 rows
+    int group;                // tiles of a taken together before the next tiles of b
+};
+
+// The t-th tile: columns of `group` tiles of a, so that what runs at one time shares operands in L2.
+__device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& ta, int& tb) {
+    const int per = a.group * a.b_tiles, g = t / per, rows = min(a.group, a.a_tiles - g * a.group), r = t - g * per;
+    tb = r / rows;
+    ta = g * a.group + (r - tb * rows);
+}
+
+template <bool NV>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThreads, 1)
+    fp4_pair_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                    const __grid_constant__ CUtensorMap as_map, const __grid_constant__ CUtensorMap bs_map,
+                    const __grid_constant__ PairArgs args) {
+    using G = PairGeo<NV>;
+    const MatmulArgs& m = args.m;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+    const uint32_t bars = base + G::kStages * G::kStage;
+    auto full = [&](int s) { return bars + 8 * s; };  // used in the first CTA
+    auto empty = [&](int s) { return bars + 8 * (G::kStages + s); };
+    const uint32_t summed = bars + 16 * G::kStages, taken = summed + 8, slot = taken + 8;
+    const int warp = int(uniform(threadIdx.x / 32)), lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, tiles = args.a_tiles * args.b_tiles;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::kStages; ++s) {
+            bar_init(full(s), 1);
+            bar_init(empty(s), 1);
+        }
+        bar_init(summed, 1);
+        bar_init(taken, 16);  // the 8 reading warps of both CTAs
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tmem_alloc_pair(slot, 512);
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+    tmem = uniform(tmem);
+    ms::wait_for_stream();
+
+    bool ok = true;
+    if (warp == 0) {
+        const bool leader = elect_one();
+        const uint32_t first = uniform(first_cta(bars));
+        int it = 0;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int ta, tb;
+            pair_tile(args, t, ta, tb);
+            const int a_row = 256 * ta + 128 * int(rank), b_row = 256 * tb + 128 * int(rank);
+            const int a_scales = (2 * ta + int(rank)) * m.scale_tiles, b_scales = 2 * tb * m.scale_tiles;
+            for (int k = 0; k < m.steps; ++k, ++it) {
+                const int s = it % G::kStages;
+                if (it >= G::kStages && !(ok = bar_wait(empty(s), (it / G::kStages - 1) & 1))) break;
+                const uint32_t st = base + s * G::kStage;
+                if (leader) {
+                    if (rank == 0) bar_expect(full(s), 2 * G::kStage);
+                    tma_2d_pair(st, &a_map, 128 * k, a_row, first + 8 * s);
+                    tma_2d_pair(st + G::kOperand, &b_map, 128 * k, b_row, first + 8 * s);
+                    tma_2d_pair(st + 2 * G::kOperand, &as_map, 0, a_scales + G::kScaleTiles * k, first + 8 * s);
+                    tma_2d_pair(st + 2 * G::kOperand + G::kAS, &bs_map, 0, b_scales + G::kScaleTiles * k, first + 8 * s);
+                    tma_2d_pair(st + 2 * G::kOperand + 2 * G::kAS, &bs_map, 0, b_scales + m.scale_tiles + G::kScaleTiles * k, first + 8 * s);
+                }
+            }
+        }
+        // nothing may still be on its way into this CTA's memory when it leaves: every stage that was
+        // filled has been used (both CTAs see that), or on giving up at least arrived (the first does)
+        for (int i = max(0, it - G::kStages); i < it; ++i) {
+            if (rank == 0) ok &= bar_wait(full(i % G::kStages), (i / G::kStages) & 1);
+            if (ok) ok &= bar_wait(empty(i % G::kStages), (i / G::kStages) & 1);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const bool leader = elect_one();
+            int it = 0, n = 0;
+            for (int t = pair; t < tiles && ok; t += pairs, ++n) {
+                if (n > 0 && !(ok = bar_wait(taken, (n - 1) & 1))) break;
+                fence_after();
+                for (int k = 0; k < m.steps; ++k, ++it) {
+                    const int s = it % G::kStages;
+                    if (!(ok = bar_wait(full(s), (it / G::kStages) & 1))) break;
+                    fence_after();
+                    const uint32_t st = base + s * G::kStage;
+                    const uint32_t sa = tmem + 256 + s * G::kScaleCols, sb = sa + 4 * G::kScaleTiles;
+                    const uint32_t da = operand_low(st), db = operand_low(st + G::kOperand), ds = scale_low(st + 2 * G::kOperand);
+                    const int products = min(4, m.k64 - 4 * k), scales = NV ? products : (products + 1) / 2;
+                    if (leader) {
+#pragma unroll
+                        for (int j = 0; j < G::kScaleTiles; ++j)
+                            if (j < scales) {
+                                copy_scales<2>(sa + 4 * j, desc(ds + 32 * j, kScaleHigh));
+                                copy_scales<2>(sb + 8 * j, desc(ds + (G::kAS >> 4) + 32 * j, kScaleHigh));
+                                copy_scales<2>(sb + 8 * j + 4, desc(ds + (2 * G::kAS >> 4) + 32 * j, kScaleHigh));
+                            }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < products)
+                                mma_fp4<NV, 2>(tmem, desc(da + 2 * j, kOperandHigh), desc(db + 2 * j, kOperandHigh),
+                                               mma_fp4_idesc<NV, 2>(256, j % 2), sa + 4 * (NV ? j : j / 2), sb + 8 * (NV ? j : j / 2),
+                                               k > 0 || j > 0);
+                        commit_pair(empty(s));
+                    }
+                }
+                if (leader) commit_pair(summed);
+            }
+        }
+    } else {
+        const float alpha = *m.ga * *m.gb;
+        const int quarter = warp % 4, half = (warp - 2) / 4;  // 32 lanes x 128 columns a warp
+        int n = 0;
+        for (int t = pair; t < tiles; t += pairs, ++n) {
+            int ta, tb;
+            pair_tile(args, t, ta, tb);
+            if (!(ok = bar_wait(summed, n & 1))) break;
+            fence_after();
+            uint32_t r[8][16];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) tmem_load16(tmem + (uint32_t(quarter) << 21) + 128 * half + 16 * c, r[c]);
+            tmem_wait_load();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_cluster(first_cta(taken));
+            const int64_t row = int64_t(256) * ta + 128 * int(rank) + 32 * quarter + lane, col = int64_t(256) * tb + 128 * half;
+            if (row < m.p_rows)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const int left = int(max(int64_t(0), min(int64_t(16), m.q_rows - col - 16 * c)));
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        v[j] = __uint_as_float(r[c][j]) * alpha;
+                        if (m.bias && j < left) v[j] += bias_at(m, col + 16 * c + j);
+                    }
+                    if (left > 0) store_run<16>(m, row, col + 16 * c, left, v);
+                }
+        }
+    }
+    __syncwarp();
+    if (!ok) atomicOr(&ep_op_status_word, 1u);
+    fence_before();
+    cluster_sync();  // no CTA leaves while the other still uses its memory or barriers
+    fence_after();
+    if (warp == 2) tmem_free_pair(tmem, 512);
+}
+
 // A product without columns: out is the bias, or zero.
 __global__ void __launch_bounds__(256) bias_kernel(const MatmulArgs a, int64_t rows, int64_t cols) {
     ms::wait_for_stream();
@@ -325,6 +504,61 @@ cudaError_t allow_smem(int dev) {
     return e;
 }
 
+// Scale tiles of 512 bytes, `box` of them at a time.
+bool scale_map(CUtensorMap* map, const ep_fp4_tensor* t, int scale_tiles, int box) {
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {128, cuuint64_t(op::div_up(t->rows, 128)) * cuuint64_t(scale_tiles)}, strides[1] = {512};
+    const cuuint32_t size[2] = {128, cuuint32_t(box)}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, t->scales, dims, strides, size, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pairs of CTAs that fit the device at one time (looked up once), after setting the kernel's shared memory.
+template <bool NV>
+cudaError_t pairs_of(int dev, int& pairs) {
+    static std::atomic<int> known[kMaxDevices];
+    pairs = known[dev].load(std::memory_order_relaxed);
+    if (pairs > 0) return cudaSuccess;
+    const auto kernel = fp4_pair_kernel<NV>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(PairGeo<NV>::kSmem));
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(PairGeo<NV>::kThreads);
+        cfg.dynamicSmemBytes = PairGeo<NV>::kSmem;
+        e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
+    }
+    if (e == cudaSuccess && pairs < 1) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess) known[dev].store(pairs, std::memory_order_relaxed);
+    return e;
+}
+
+template <bool NV>
+int run_pairs(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int dev, cudaStream_t st) {
+    CUtensorMap a_map, b_map, as_map, bs_map;
+    if (!operand_map(&a_map, a, 128) || !operand_map(&b_map, b, 128) ||
+        !scale_map(&as_map, a, args.scale_tiles, PairGeo<NV>::kScaleTiles) ||
+        !scale_map(&bs_map, b, args.scale_tiles, PairGeo<NV>::kScaleTiles))
+        return set_error(EP_ERR_CUDA, "ep_fp4_matmul: tensor map");
+    PairArgs p = {args};
+    p.m.p_rows = a->rows;
+    p.m.q_rows = b->rows;
+    p.a_tiles = int(op::div_up(a->rows, 256));
+    p.b_tiles = int(op::div_up(b->rows, 256));
+    p.group = 8;
+    if (int64_t(p.a_tiles) * p.b_tiles > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: too many tiles");
+    int pairs = 0;
+    cudaError_t e = pairs_of<NV>(dev, pairs);
+    if (e == cudaSuccess) {
+        pairs = std::min(pairs, p.a_tiles * p.b_tiles);
+        e = op::launch(fp4_pair_kernel<NV>, dim3(unsigned(2 * pairs)), dim3(PairGeo<NV>::kThreads), PairGeo<NV>::kSmem, st, a_map, b_map,
+                       as_map, bs_map, p);
+    }
+    if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_matmul: ") + cudaGetErrorString(e));
+    return EP_OK;
+}
+
 template <int NT, bool SWAP, bool NV>
 int run_tiles(const ep_fp4_tensor* p, const ep_fp4_tensor* q, MatmulArgs a, int split, int dev, cudaStream_t st) {
     using G = Geo<NT, NV>;
@@ -371,7 +605,7 @@ int matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& arg
     if (m <= 64) return run_tiles<64, true, NV>(b, a, args, split(n_tiles), dev, st);
     if (m <= 128) return run_tiles<128, true, NV>(b, a, args, split(n_tiles), dev, st);
     const int64_t m_tiles = op::div_up(m, 128);
-    if (m_tiles * op::div_up(n, 256) >= sms) return run_tiles<256, false, NV>(a, b, args, 1, dev, st);
+    if (m_tiles * op::div_up(n, 256) >= sms) return run_pairs<NV>(a, b, args, dev, st);
     return run_tiles<128, false, NV>(a, b, args, split(m_tiles * n_tiles), dev, st);
 }
 

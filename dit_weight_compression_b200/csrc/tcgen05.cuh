@@ -12,6 +12,15 @@ namespace tc {
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
+// One lane of a converged warp.  The warps that issue copies and products run warp-uniform code around
+// it, so that addresses and descriptors stay in uniform registers, which those instructions read.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // ---- mbarriers -----------------------------------------------------------------------------------
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -51,6 +60,21 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// The address of the same place in the first CTA of the cluster.
+__device__ __forceinline__ uint32_t first_cta(uint32_t smem) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem));
+    return a;
+}
+// For a CTA of a pair: into its own memory, arriving on a barrier of either CTA (a cluster address).
+__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
 // ---- tensor memory -----------------------------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t columns) {  // a whole warp
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(columns) : "memory");
@@ -58,6 +82,13 @@ __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t columns)
 }
 __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {  // the same warp
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t smem_slot, uint32_t columns) {  // a warp of each CTA
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_slot), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t tmem, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
 }
 // 32 lanes (this warp's quarter) x 16 columns.
 __device__ __forceinline__ void tmem_load16(uint32_t tmem, uint32_t (&r)[16]) {
@@ -72,48 +103,68 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // ---- products ------------------------------------------------------------------------------------------
-// Descriptor of a K-major operand tile in shared memory, rows of 128 bytes in the 128-byte swizzle:
-// groups of 8 rows are 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t smem) {
-    return uint64_t((smem & 0x3ffffu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
-           (uint64_t(2) << 61);
-}
-// Descriptor of a 512-byte scale tile, 32 rows of 16 bytes, no swizzle: groups of 8 rows are 128
-// bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {
-    return uint64_t((smem & 0x3ffffu) >> 4) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
-}
+// Descriptors: the low word holds the address (in 16 bytes), the high word is fixed.
+__device__ __forceinline__ uint64_t desc(uint32_t low, uint32_t high) { return (uint64_t(high) << 32) | low; }
+// A K-major operand tile in shared memory, rows of 128 bytes in the 128-byte swizzle: groups of 8 rows are
+// 1024 bytes apart.
+constexpr uint32_t kOperandHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand_low(uint32_t smem) { return ((smem & 0x3ffffu) >> 4) | (1u << 16); }
+// A 512-byte scale tile, 32 rows of 16 bytes, no swizzle: groups of 8 rows are 128 bytes apart.
+constexpr uint32_t kScaleHigh = (128 >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t scale_low(uint32_t smem) { return (smem & 0x3ffffu) >> 4; }
 // One scale tile to 4 tensor memory columns, the same in every quarter of the lanes.
+template <int CTAS = 1>
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    if constexpr (CTAS == 1) asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    else asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
-// D[128][n] (+)= A[128][64] * B[n][64] with E2M1 elements; blocks of 16 with E4M3 scales (NV) or of
-// 32 with E8M0 scales.
-template <bool NV>
+// D[128 CTAS][n] (+)= A[128 CTAS][64] * B[n][64] with E2M1 elements; blocks of 16 with E4M3 scales (NV) or
+// of 32 with E8M0 scales.  Of a pair, each CTA holds 128 rows of A and D and half of B's rows, with the
+// scales of its own A and of all of B.
+template <bool NV, int CTAS = 1>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
-    if constexpr (NV)
+    if constexpr (NV && CTAS == 1) {
         asm volatile(
             "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
             " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(add))
             : "memory");
-    else
+    } else if constexpr (CTAS == 1) {
         asm volatile(
             "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
             " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
             "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(add))
             : "memory");
+    } else if constexpr (NV) {
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(add))
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+            " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(uint32_t(add))
+            : "memory");
+    }
 }
-// Instruction descriptor of mma_fp4: E2M1 operands, both K-major, M = 128.  `half` picks which two of
-// a column's four scales a product of 64 elements in blocks of 32 uses.
-template <bool NV>
+// Instruction descriptor of mma_fp4: E2M1 operands, both K-major.  `half` picks which two of a column's
+// four scales a product of 64 elements in blocks of 32 uses.
+template <bool NV, int CTAS = 1>
 __host__ __device__ constexpr uint32_t mma_fp4_idesc(int n, int half) {
     return (uint32_t(NV ? 0 : 2 * half) << 4) | (1u << 7) | (1u << 10) | (uint32_t(n / 8) << 17) | (uint32_t(NV ? 0 : 1) << 23) |
-           (uint32_t(128 / 16) << 24) | (uint32_t(NV ? 0 : 2 * half) << 29);
+           (uint32_t(128 * CTAS / 16) << 24) | (uint32_t(NV ? 0 : 2 * half) << 29);
 }
 // Arrives on the barrier when every product and scale copy issued so far by this thread is done.
 __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// The same on the barrier at this address of both CTAs of a pair.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"(uint16_t(3))
+                 : "memory");
 }
 
 // ---- clusters --------------------------------------------------------------------------------------------
@@ -124,6 +175,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Arrives on a barrier of any CTA of the cluster.
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // A float4 / float of the shared memory of CTA `rank` of the cluster, at this CTA's own address.
 __device__ __forceinline__ float4 peer_load4(uint32_t smem, uint32_t rank) {
