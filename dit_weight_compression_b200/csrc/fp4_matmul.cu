@@ -21,39 +21,37 @@ constexpr int kThreads = 192;   // warp 0 copies, warp 1 issues products, warps 
 __device__ uint32_t ep_op_status_word;
 
 struct MatmulArgs {
-    const uint8_t* p_scales;   // of the operand whose rows are the tensor core's 128 lanes
-    const uint8_t* q_scales;   // of the operand whose rows are its columns
+    const uint8_t* a_scales;
+    const uint8_t* b_scales;
     const float* ga;
     const float* gb;
     const void* bias;
     void* out;
     int64_t stride;            // of out's rows
-    int64_t p_rows, q_rows;
+    int64_t rows, cols;        // of out
     int scale_tiles;           // 512-byte scale tiles along K
     int steps;                 // stages along K
     int k64;                   // products of 64 along K
-    int p_tiles;
+    int n_tiles;               // tiles of 128 rows of b
     int out_dtype;
-    bool vec;                  // out's rows are 16-byte aligned
+    int width;                 // alignment of out's rows: 16, 8 or 4 bytes, or 1 for their elements'
 };
 
-// Tile sizes, stage layout and tensor memory columns of a variant with tiles of NT columns.
+// Tile sizes, stage layout and tensor memory columns of a variant with tiles of NT tokens.
 template <int NT, bool NV>
 struct Geo {
     static constexpr int kScaleTiles = NV ? 4 : 2;            // scale tiles of 128 rows x one stage
-    static constexpr int kQBlocks = (NT + 127) / 128;
-    static constexpr int kP = 128 * 128, kQ = NT * 128;       // bytes of the operands' stage tiles
-    static constexpr int kPS = kScaleTiles * 512, kQS = kQBlocks * kScaleTiles * 512;
-    static constexpr int kStage = kP + kQ + kPS + kQS;
-    static constexpr bool kPair = NT < 256;                   // two CTAs share an SM
-    static constexpr int kBudget = (kPair ? 113 : 226) * 1024;
-    static constexpr int kStages = (kBudget - 2048) / kStage < 8 ? (kBudget - 2048) / kStage : 8;
+    static constexpr int kB = 128 * 128, kA = NT * 128;       // bytes of the operands' stage tiles
+    static constexpr int kS = kScaleTiles * 512;              // and of each one's scales
+    static constexpr int kStage = kB + kA + 2 * kS;
+    static constexpr int kBudget = 113 * 1024 - 2048;         // two CTAs share an SM
+    static constexpr int kStages = kBudget / kStage;
     static constexpr int kSum = NT < 32 ? 32 : NT;            // accumulator columns
-    static constexpr int kScaleCols = 4 * kScaleTiles * (1 + kQBlocks);  // of one stage
-    static constexpr int kColumns = kSum + kStages * kScaleCols <= 256 ? 256 : 512;
+    static constexpr int kScaleCols = 8 * kScaleTiles;        // of one stage
+    static constexpr int kColumns = 256;
     static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 256;
     static_assert(kStages >= 3, "a pipeline of at least three stages");
-    static_assert(kSum + kStages * kScaleCols <= (kPair ? 256 : 512), "tensor memory");
+    static_assert(kSum + kStages * kScaleCols <= kColumns, "tensor memory");
     static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024-byte boundaries");
     static_assert(kStages * kStage >= 128 * NT * 4, "partial sums fit the stages");
 };
@@ -65,46 +63,43 @@ __device__ __forceinline__ float bias_at(const MatmulArgs& a, int64_t n) {
     return __half2float(static_cast<const __half*>(a.bias)[n]);
 }
 
-// `n` neighbouring elements (N at most) of row i from column j on.
-template <int N>
-__device__ __forceinline__ void store_run(const MatmulArgs& a, int64_t i, int64_t j, int n, const float* v) {
+// The first n of four neighbouring elements of row i from column j (a multiple of 4) on.
+__device__ __forceinline__ void store4(const MatmulArgs& a, int64_t i, int64_t j, int n, const float* v) {
     const int64_t at = i * a.stride + j;
     if (a.out_dtype == EP_F32) {
         float* o = static_cast<float*>(a.out) + at;
-        if (a.vec && n == N) {
-#pragma unroll
-            for (int k = 0; k < N; k += 4) *reinterpret_cast<float4*>(o + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        if (n == 4 && a.width == 16) {
+            *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
         } else {
 #pragma unroll
-            for (int k = 0; k < N; ++k)
+            for (int k = 0; k < 4; ++k)
                 if (k < n) o[k] = v[k];
         }
         return;
     }
-    uint32_t w[N / 2];
+    uint32_t w[2];
 #pragma unroll
-    for (int k = 0; k < N / 2; ++k)
+    for (int k = 0; k < 2; ++k)
         w[k] = a.out_dtype == EP_BF16 ? ms::pack2<EP_BF16>(v[2 * k], v[2 * k + 1]) : ms::pack2<EP_FP16>(v[2 * k], v[2 * k + 1]);
     uint16_t* o = static_cast<uint16_t*>(a.out) + at;
-    if (a.vec && n == N) {
-        if constexpr (N == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
-        else
-#pragma unroll
-            for (int k = 0; k < N; k += 8)
-                *reinterpret_cast<uint4*>(o + k) = make_uint4(w[k / 2], w[k / 2 + 1], w[k / 2 + 2], w[k / 2 + 3]);
+    if (n == 4 && a.width >= 8) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
-        for (int k = 0; k < N; ++k)
+        for (int k = 0; k < 4; ++k)
             if (k < n) o[k] = uint16_t(w[k / 2] >> (16 * (k % 2)));
     }
 }
 
-// One cluster per tile of 128 rows of p x NT rows of q; its CTAs share the stages along K and then
-// the tile's columns: each adds up its share of columns over all CTAs' partial sums, in rank order.
-// SWAP: p holds b's rows (out's columns) and q a's; else p holds a's rows.
-template <int NT, bool SWAP, bool NV>
-__global__ void __launch_bounds__(kThreads) fp4_matmul_kernel(const __grid_constant__ CUtensorMap p_map,
-                                                               const __grid_constant__ CUtensorMap q_map, const MatmulArgs a) {
+// ---- short products -------------------------------------------------------------------------------
+// One cluster per tile of 128 rows of b (the tensor core's lanes, so that few tokens do not leave them
+// idle) x NT tokens; its CTAs share the stages along K and then the tile's tokens: each adds up its share
+// of tokens over all CTAs' partial sums, in rank order, and writes runs of 128 outputs.  Two CTAs share an
+// SM: the copies of one go on while the other starts or ends.
+template <int NT, bool NV>
+__global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_constant__ CUtensorMap b_map,
+                                                                 const __grid_constant__ CUtensorMap a_map,
+                                                                 const __grid_constant__ MatmulArgs a) {
     using G = Geo<NT, NV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -117,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) fp4_matmul_kernel(const __grid_const
     uint32_t ranks, rank = cluster_rank();
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
     const int tile = int(blockIdx.x / ranks);
-    const int p0 = (tile % a.p_tiles) * 128, q0 = (tile / a.p_tiles) * NT;
+    const int n0 = (tile % a.n_tiles) * 128, m0 = (tile / a.n_tiles) * NT;
     const int k0 = int(int64_t(a.steps) * rank / ranks), steps = int(int64_t(a.steps) * (rank + 1) / ranks) - k0;
 
     if (threadIdx.x == 0) {
@@ -139,24 +134,20 @@ __global__ void __launch_bounds__(kThreads) fp4_matmul_kernel(const __grid_const
 
     bool ok = true;
     if (warp == 0) {
-        const bool leader = elect_one(), second = G::kQBlocks == 2 && q0 + 128 < a.q_rows;
+        const bool leader = elect_one();
         int issued = 0;
         for (int it = 0; it < steps; ++it) {
             const int s = it % G::kStages, k = k0 + it;
             if (it >= G::kStages && !(ok = bar_wait(empty(s), (it / G::kStages - 1) & 1))) break;
-            const int tiles = min(G::kScaleTiles, a.scale_tiles - k * G::kScaleTiles);
+            const int bytes = 512 * min(G::kScaleTiles, a.scale_tiles - k * G::kScaleTiles);
             const uint32_t st = base + s * G::kStage;
             const int64_t at = int64_t(k) * G::kScaleTiles;
             if (leader) {
-                bar_expect(full(s), G::kP + G::kQ + 512 * tiles * (second ? 3 : 2));
-                tma_2d(st, &p_map, 128 * k, p0, full(s));
-                tma_2d(st + G::kP, &q_map, 128 * k, q0, full(s));
-                bulk_copy(st + G::kP + G::kQ, a.p_scales + (int64_t(p0 / 128) * a.scale_tiles + at) * 512, 512 * tiles, full(s));
-#pragma unroll
-                for (int b = 0; b < G::kQBlocks; ++b)
-                    if (b == 0 || second)
-                        bulk_copy(st + G::kP + G::kQ + G::kPS * (1 + b),
-                                  a.q_scales + ((int64_t(q0) / 128 + b) * a.scale_tiles + at) * 512, 512 * tiles, full(s));
+                bar_expect(full(s), G::kB + G::kA + 2 * bytes);
+                tma_2d(st, &b_map, 128 * k, n0, full(s));
+                bulk_copy(st + G::kB + G::kA, a.b_scales + (int64_t(n0 / 128) * a.scale_tiles + at) * 512, bytes, full(s));
+                tma_2d(st + G::kB, &a_map, 128 * k, m0, full(s));
+                bulk_copy(st + G::kB + G::kA + G::kS, a.a_scales + (int64_t(m0 / 128) * a.scale_tiles + at) * 512, bytes, full(s));
             }
             issued = it + 1;
         }
@@ -169,24 +160,22 @@ __global__ void __launch_bounds__(kThreads) fp4_matmul_kernel(const __grid_const
             if (!(ok = bar_wait(full(s), (it / G::kStages) & 1))) break;
             fence_after();
             const uint32_t st = base + s * G::kStage;
-            const uint32_t sp = tmem + G::kSum + s * G::kScaleCols, sq = sp + 4 * G::kScaleTiles;
-            const uint32_t da = operand_low(st), db = operand_low(st + G::kP), ds = scale_low(st + G::kP + G::kQ);
+            const uint32_t sb = tmem + G::kSum + s * G::kScaleCols, sa = sb + 4 * G::kScaleTiles;
+            const uint32_t db = operand_low(st), da = operand_low(st + G::kB), ds = scale_low(st + G::kB + G::kA);
             const int products = min(4, a.k64 - 4 * (k0 + it)), tiles = NV ? products : (products + 1) / 2;
             if (leader) {
 #pragma unroll
                 for (int t = 0; t < G::kScaleTiles; ++t)
                     if (t < tiles) {
-                        copy_scales(sp + 4 * t, desc(ds + 32 * t, kScaleHigh));
-#pragma unroll
-                        for (int b = 0; b < G::kQBlocks; ++b)
-                            copy_scales(sq + 4 * (t * G::kQBlocks + b), desc(ds + (G::kPS * (1 + b) >> 4) + 32 * t, kScaleHigh));
+                        copy_scales(sb + 4 * t, desc(ds + 32 * t, kScaleHigh));
+                        copy_scales(sa + 4 * t, desc(ds + (G::kS >> 4) + 32 * t, kScaleHigh));
                     }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (j < products) {
                         const int t = NV ? j : j / 2;
-                        mma_fp4<NV>(tmem, desc(da + 2 * j, kOperandHigh), desc(db + 2 * j, kOperandHigh), mma_fp4_idesc<NV>(NT, j % 2),
-                                    sp + 4 * t, sq + 4 * G::kQBlocks * t, it > 0 || j > 0);
+                        mma_fp4<NV>(tmem, desc(db + 2 * j, kOperandHigh), desc(da + 2 * j, kOperandHigh), mma_fp4_idesc<NV>(NT, j % 2),
+                                    sb + 4 * t, sa + 4 * t, it > 0 || j > 0);
                     }
                 commit(empty(s));
             }
@@ -199,81 +188,42 @@ __global__ void __launch_bounds__(kThreads) fp4_matmul_kernel(const __grid_const
     fence_after();
 
     const float alpha = *a.ga * *a.gb;
-    const int64_t lane0 = p0, col0 = q0;
-    if (ranks == 1 && !SWAP) {
-        if (warp >= 2) {
-            const int row = (warp % 4) * 32 + lane;
-            for (int c = 0; c < NT; c += 16) {
-                uint32_t r[16];
-                __syncwarp();
-                tmem_load16(tmem + (uint32_t(warp % 4) << 21) + c, r);
-                tmem_wait_load();
-                float v[16];
+    float* part = reinterpret_cast<float*>(smem);  // [token][row of b]
+    if (warp >= 2) {
+        const int row = (warp % 4) * 32 + lane;
+        for (int c = 0; c < NT; c += 16) {
+            uint32_t r[16];
+            tmem_load16(tmem + (uint32_t(warp % 4) << 21) + c, r);
+            tmem_wait_load();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    v[j] = __uint_as_float(r[j]) * alpha;
-                    if (a.bias && col0 + c + j < a.q_rows) v[j] += bias_at(a, col0 + c + j);
-                }
-                const int n = int(max(int64_t(0), min(int64_t(16), a.q_rows - col0 - c)));
-                if (ok && lane0 + row < a.p_rows && n > 0) store_run<16>(a, lane0 + row, col0 + c, n, v);
-            }
+            for (int j = 0; j < 16; ++j) part[(c + j) * 128 + row] = __uint_as_float(r[j]);
         }
-        fence_before();
-        __syncthreads();
-    } else {
-        float* part = reinterpret_cast<float*>(smem);  // [column][lane]
-        if (warp >= 2) {
-            const int row = (warp % 4) * 32 + lane;
-            for (int c = 0; c < NT; c += 16) {
-                uint32_t r[16];
-                __syncwarp();
-                tmem_load16(tmem + (uint32_t(warp % 4) << 21) + c, r);
-                tmem_wait_load();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) part[(c + j) * 128 + row] = __uint_as_float(r[j]);
-            }
-        }
-        fence_before();
-        __syncwarp();
-        cluster_sync();
-        // this CTA's columns: whole groups of 8 where 8 neighbours are stored at once
-        constexpr int kGroup = SWAP ? 1 : 8;
-        const int c0 = NT / kGroup * int(rank) / int(ranks) * kGroup, c1 = NT / kGroup * (int(rank) + 1) / int(ranks) * kGroup;
-        if (SWAP) {
-            const int64_t n0 = lane0 + 4 * lane;
-            const int n = int(max(int64_t(0), min(int64_t(4), a.p_rows - n0)));
-            float bias[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) bias[j] = j < n ? bias_at(a, n0 + j) : 0.0f;
-            for (int c = c0 + warp; c < c1 && col0 + c < a.q_rows; c += kThreads / 32) {
-                float v[4] = {};
-                for (uint32_t r = 0; r < ranks; ++r) {
-                    const float4 f = peer_load4(base + 4 * (c * 128 + 4 * lane), r);
-                    v[0] += f.x;
-                    v[1] += f.y;
-                    v[2] += f.z;
-                    v[3] += f.w;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = v[j] * alpha + bias[j];
-                if (ok && n > 0) store_run<4>(a, col0 + c, n0, n, v);
-            }
-        } else if (threadIdx.x < 128) {
-            for (int c = c0; c < c1 && col0 + c < a.q_rows; c += 8) {
-                float v[8] = {};
-                for (uint32_t r = 0; r < ranks; ++r)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += peer_load(base + 4 * ((c + j) * 128 + int(threadIdx.x)), r);
-                const int n = int(min(int64_t(8), a.q_rows - col0 - c));
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = v[j] * alpha + (j < n ? bias_at(a, col0 + c + j) : 0.0f);
-                if (ok && lane0 + threadIdx.x < a.p_rows) store_run<8>(a, lane0 + threadIdx.x, col0 + c, n, v);
-            }
-        }
-        __syncwarp();
-        cluster_sync();  // no CTA leaves while another reads its sums
-        fence_after();
     }
+    fence_before();
+    __syncwarp();
+    cluster_sync();
+    const int c0 = NT * int(rank) / int(ranks), c1 = NT * (int(rank) + 1) / int(ranks);
+    const int64_t col = int64_t(n0) + 4 * lane;
+    const int n = int(max(int64_t(0), min(int64_t(4), a.cols - col)));
+    float bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bias[j] = j < n ? bias_at(a, col + j) : 0.0f;
+    for (int c = c0 + warp; c < c1 && int64_t(m0) + c < a.rows; c += kThreads / 32) {
+        float v[4] = {};
+        for (uint32_t r = 0; r < ranks; ++r) {
+            const float4 f = peer_load4(base + 4 * (c * 128 + 4 * lane), r);
+            v[0] += f.x;
+            v[1] += f.y;
+            v[2] += f.z;
+            v[3] += f.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = v[j] * alpha + bias[j];
+        if (ok && n > 0) store4(a, int64_t(m0) + c, col, n, v);
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another reads its sums
+    fence_after();
     if (!ok) atomicOr(&ep_op_status_word, 1u);
     if (warp == 2) tmem_free(tmem, G::kColumns);
 }
@@ -293,7 +243,8 @@ struct PairGeo {
     static constexpr int kStage = 2 * kOperand + kAS + kBS;
     static constexpr int kStages = 5;
     static constexpr int kScaleCols = 4 * kScaleTiles * 3;
-    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 256;
+    static constexpr int kOut = 4096;                          // a reading warp's outputs on their way
+    static constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + 8 * kOut + 256;
     static constexpr int kThreads = 320;
     static_assert(256 + kStages * kScaleCols <= 512, "tensor memory");
     static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -304,6 +255,53 @@ struct PairArgs {
     int a_tiles, b_tiles;     // tiles of 256 rows
     int group;                // tiles of a taken together before the next tiles of b
 };
+
+// A warp's 32 rows x 128 bytes of outputs, one row a lane in registers, to memory: through 4 KB of shared
+// memory (16-byte pieces, exclusive-ored with the row against bank conflicts), so that the lanes write
+// neighbouring bytes of a row.  A lane storing its own row's 16 bytes took 7 us of a 256 x 256 bf16 tile;
+// this way a tile of 256 columns of K or more hides it.
+__device__ __forceinline__ void store_rows(const MatmulArgs& m, uint32_t buf, int lane, int64_t row0, int64_t col, const uint32_t* w) {
+    const int size = m.out_dtype == EP_F32 ? 4 : 2, per = 128 / size;  // columns
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + 128 * lane + 16 * (i ^ (lane & 7))), "r"(w[4 * i]),
+                     "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                     : "memory");
+    __syncwarp();
+    const int rows = int(max(int64_t(0), min(int64_t(32), m.rows - row0))), cols = int(max(int64_t(0), min(int64_t(per), m.cols - col)));
+    uint8_t* out = static_cast<uint8_t*>(m.out) + (row0 * m.stride + col) * size;
+    if (m.width == 16 && cols == per) {
+        const int c = lane % 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + lane / 8;
+            uint4 u;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                         : "r"(buf + 128 * r + 16 * (c ^ (r & 7))));
+            if (r < rows) *reinterpret_cast<uint4*>(out + r * m.stride * size + 16 * c) = u;
+        }
+        return;
+    }
+    // rows that start anywhere, or the last columns
+    for (int r = 0; r < rows; ++r) {
+        const uint32_t line = buf + 128 * r;
+        if (size == 4 || (m.width >= 4 && cols % 2 == 0)) {
+            uint32_t u;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(line + 16 * ((lane / 4) ^ (r & 7)) + 4 * (lane % 4)));
+            if (4 * lane < cols * size) *reinterpret_cast<uint32_t*>(out + r * m.stride * size + 4 * lane) = u;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int c = lane + 32 * e;
+                uint16_t u;
+                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(line + 16 * ((c / 8) ^ (r & 7)) + 2 * (c % 8)));
+                if (c < cols) *reinterpret_cast<uint16_t*>(out + r * m.stride * size + 2 * c) = u;
+            }
+        }
+    }
+}
 
 // The t-th tile: columns of `group` tiles of a, so that what runs at one time shares operands in L2.
 __device__ __forceinline__ void pair_tile(const PairArgs& a, int t, int& ta, int& tb) {
@@ -321,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
     const MatmulArgs& m = args.m;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
-    const uint32_t bars = base + G::kStages * G::kStage;
+    const uint32_t out_bufs = base + G::kStages * G::kStage, bars = out_bufs + 8 * G::kOut;
     auto full = [&](int s) { return bars + 8 * s; };  // used in the first CTA
     auto empty = [&](int s) { return bars + 8 * (G::kStages + s); };
     const uint32_t summed = bars + 16 * G::kStages, taken = summed + 8, slot = taken + 8;
@@ -429,19 +427,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive_cluster(first_cta(taken));
-            const int64_t row = int64_t(256) * ta + 128 * int(rank) + 32 * quarter + lane, col = int64_t(256) * tb + 128 * half;
-            if (row < m.p_rows)
+            const int64_t row0 = int64_t(256) * ta + 128 * int(rank) + 32 * quarter, col = int64_t(256) * tb + 128 * half;
+            const uint32_t buf = out_bufs + (warp - 2) * G::kOut;
+            if (m.bias) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const int left = int(max(int64_t(0), min(int64_t(16), m.q_rows - col - 16 * c)));
-                    float v[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        v[j] = __uint_as_float(r[c][j]) * alpha;
-                        if (m.bias && j < left) v[j] += bias_at(m, col + 16 * c + j);
-                    }
-                    if (left > 0) store_run<16>(m, row, col + 16 * c, left, v);
+                for (int c = 0; c < 128; ++c) {
+                    const float v = __uint_as_float(r[c / 16][c % 16]) * alpha + (col + c < m.cols ? bias_at(m, col + c) : 0.0f);
+                    r[c / 16][c % 16] = __float_as_uint(v);
                 }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 128; ++c) r[c / 16][c % 16] = __float_as_uint(__uint_as_float(r[c / 16][c % 16]) * alpha);
+            }
+            if (m.out_dtype == EP_F32) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (col + 32 * c < m.cols) store_rows(m, buf, lane, row0, col + 32 * c, &r[2 * c][0]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 64; ++c) {
+                    const float lo = __uint_as_float(r[c / 8][2 * (c % 8)]), hi = __uint_as_float(r[c / 8][2 * (c % 8) + 1]);
+                    r[c / 16][c % 16] = m.out_dtype == EP_BF16 ? ms::pack2<EP_BF16>(lo, hi) : ms::pack2<EP_FP16>(lo, hi);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (col + 64 * c < m.cols) store_rows(m, buf, lane, row0, col + 64 * c, &r[2 * c][0]);
+            }
         }
     }
     __syncwarp();
@@ -494,11 +505,11 @@ bool operand_map(CUtensorMap* map, const ep_fp4_tensor* t, int box_rows) {
 }
 
 // Sets the shared memory size of a variant's kernel, once per device.
-template <int NT, bool SWAP, bool NV>
+template <int NT, bool NV>
 cudaError_t allow_smem(int dev) {
     static std::atomic<bool> done[kMaxDevices];
     if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(fp4_matmul_kernel<NT, SWAP, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(fp4_split_kernel<NT, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                int(Geo<NT, NV>::kSmem));
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
     return e;
@@ -542,8 +553,6 @@ int run_pairs(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& 
         !scale_map(&bs_map, b, args.scale_tiles, PairGeo<NV>::kScaleTiles))
         return set_error(EP_ERR_CUDA, "ep_fp4_matmul: tensor map");
     PairArgs p = {args};
-    p.m.p_rows = a->rows;
-    p.m.q_rows = b->rows;
     p.a_tiles = int(op::div_up(a->rows, 256));
     p.b_tiles = int(op::div_up(b->rows, 256));
     p.group = 8;
@@ -559,19 +568,17 @@ int run_pairs(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& 
     return EP_OK;
 }
 
-template <int NT, bool SWAP, bool NV>
-int run_tiles(const ep_fp4_tensor* p, const ep_fp4_tensor* q, MatmulArgs a, int split, int dev, cudaStream_t st) {
+template <int NT, bool NV>
+int run_split(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int sms, int dev, cudaStream_t st) {
     using G = Geo<NT, NV>;
-    CUtensorMap p_map, q_map;
-    if (!operand_map(&p_map, p, 128) || !operand_map(&q_map, q, NT)) return set_error(EP_ERR_CUDA, "ep_fp4_matmul: tensor map");
-    a.p_scales = static_cast<const uint8_t*>(p->scales);
-    a.q_scales = static_cast<const uint8_t*>(q->scales);
-    a.p_rows = p->rows;
-    a.q_rows = q->rows;
-    a.p_tiles = int(op::div_up(p->rows, 128));
-    const int64_t grid = int64_t(a.p_tiles) * op::div_up(q->rows, NT) * split;
+    CUtensorMap b_map, a_map;
+    if (!operand_map(&b_map, b, 128) || !operand_map(&a_map, a, NT)) return set_error(EP_ERR_CUDA, "ep_fp4_matmul: tensor map");
+    // CTAs of one tile: as many as fill two CTAs an SM, at most 8 and one stage each
+    const int64_t tiles = int64_t(args.n_tiles) * op::div_up(a->rows, NT);
+    const int split = int(std::max<int64_t>(1, std::min<int64_t>({8, args.steps, 2 * int64_t(sms) / tiles})));
+    const int64_t grid = tiles * split;
     if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: too many tiles");
-    cudaError_t e = allow_smem<NT, SWAP, NV>(dev);
+    cudaError_t e = allow_smem<NT, NV>(dev);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(grid));
@@ -586,7 +593,7 @@ int run_tiles(const ep_fp4_tensor* p, const ep_fp4_tensor* q, MatmulArgs a, int 
         at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 2;
-        e = cudaLaunchKernelEx(&cfg, fp4_matmul_kernel<NT, SWAP, NV>, p_map, q_map, a);
+        e = cudaLaunchKernelEx(&cfg, fp4_split_kernel<NT, NV>, b_map, a_map, args);
     }
     if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_matmul: ") + cudaGetErrorString(e));
     return EP_OK;
@@ -594,19 +601,12 @@ int run_tiles(const ep_fp4_tensor* p, const ep_fp4_tensor* q, MatmulArgs a, int 
 
 template <bool NV>
 int matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int sms, int dev, cudaStream_t st) {
-    const int64_t m = a->rows, n = b->rows;
-    // CTAs of one tile: as many as fill two CTAs an SM, at most 8 and one stage each
-    auto split = [&](int64_t tiles) {
-        return int(std::max<int64_t>(1, std::min<int64_t>({8, args.steps, 2 * int64_t(sms) / std::max<int64_t>(1, tiles)})));
-    };
-    const int64_t n_tiles = op::div_up(n, 128);
-    if (m <= 16) return run_tiles<16, true, NV>(b, a, args, split(n_tiles), dev, st);
-    if (m <= 32) return run_tiles<32, true, NV>(b, a, args, split(n_tiles), dev, st);
-    if (m <= 64) return run_tiles<64, true, NV>(b, a, args, split(n_tiles), dev, st);
-    if (m <= 128) return run_tiles<128, true, NV>(b, a, args, split(n_tiles), dev, st);
-    const int64_t m_tiles = op::div_up(m, 128);
-    if (m_tiles * op::div_up(n, 256) >= sms) return run_pairs<NV>(a, b, args, dev, st);
-    return run_tiles<128, false, NV>(a, b, args, split(m_tiles * n_tiles), dev, st);
+    const int64_t m = a->rows;
+    if (m <= 16) return run_split<16, NV>(a, b, args, sms, dev, st);
+    if (m <= 32) return run_split<32, NV>(a, b, args, sms, dev, st);
+    if (m <= 64) return run_split<64, NV>(a, b, args, sms, dev, st);
+    if (op::div_up(m, 128) * op::div_up(b->rows, 256) >= sms) return run_pairs<NV>(a, b, args, dev, st);
+    return run_split<128, NV>(a, b, args, sms, dev, st);
 }
 
 }  // namespace
@@ -642,7 +642,12 @@ extern "C" int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, con
     args.out = out->data;
     args.stride = out->row_stride;
     args.out_dtype = out->dtype;
-    args.vec = op::aligned(out->data, 16) && (out->row_stride * es) % 16 == 0;
+    args.rows = out->rows;
+    args.cols = out->cols;
+    args.a_scales = static_cast<const uint8_t*>(a->scales);
+    args.b_scales = static_cast<const uint8_t*>(b->scales);
+    args.n_tiles = int(op::div_up(b->rows, 128));
+    args.width = op::access_width(out->data, out->row_stride * es);
     args.steps = int(op::div_up(a->cols, kStepK));
     args.k64 = int(op::div_up(a->cols, 64));
     args.scale_tiles = int(op::div_up(op::fp4_blocks(a->format, a->cols), 4));
