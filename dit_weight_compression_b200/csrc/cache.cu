@@ -12,8 +12,14 @@ namespace {
 
 using namespace ms;
 
+// Two variants of each kernel.  The common one serves rows of up to 256 elements in whole eights, 16-byte
+// aligned outside the cache: a lane has 16 elements, so that the row's addresses, maximum and scale, which
+// cost as much as 8 elements, are shared by more (per 8 elements and lane 228 -> 112 instructions in an
+// int8 write, 120 -> 61 in an fp8 read, of the 133 that copying at the memory's rate leaves time for).
+// The other serves every head up to 1024 elements, 8 a lane, at any alignment.
 constexpr int kThreads = 256;
 constexpr int kMaxHeadDim = 1024;
+constexpr int kMaxFastDim = 256;
 constexpr int kLaunchTokens = 4096;  // tokens of one write launch
 constexpr int kMaxWriteTokens = 8;   // most tokens of one block of a write
 constexpr int kMaxReadTokens = 64;   // most tokens of one block of a read
@@ -119,75 +125,33 @@ __device__ __forceinline__ uint2 e4m3_payload(const Raw8<DT>& v, float inv) {
     return make_uint2(w[0], w[1]);
 }
 
-// The payload (and by its first lane the scale) of one row, of which this lane holds chunks of 8
-// elements `lane`, `lane + LANES`, ...; they are zeros past the row's end.
-template <int DT, int FMT, int LANES, int NC>
-__device__ __forceinline__ void write_row(const CacheView& c, uint8_t* data, uint8_t* scales, int lane, const Raw8<DT>* v, bool live) {
-    if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
-        uint32_t bits = 0;
-#pragma unroll
-        for (int k = 0; k < NC; ++k) bits = max(bits, abs_max8<DT>(v[k]));
-        bits = lanes_max<LANES>(bits);
-        const bool fine = bits < AbsBits<DT>::kInf;
-        const float amax = abs_value<DT>(bits);
-        float s, inv;
-        if constexpr (FMT == EP_FP8_E4M3) {
-            const int e = e4m3_row_exponent(amax);
-            s = pow2f(e);
-            inv = pow2f(-e);
-        } else {
-            s = amax >= 0x1p-100f ? __fmul_rn(amax, 1.0f / 127.0f) : 0.0f;
-            inv = s > 0.0f ? reciprocal_near(s) : 0.0f;
-        }
-        if (!fine) s = __int_as_float(0x7fc00000);
-        if (!live) return;
-        if (lane == 0) *reinterpret_cast<float*>(scales) = s;
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int at = 8 * (lane + k * LANES);
-            if (at >= c.head_dim) break;
-            uint2 w = make_uint2(0, 0);
-            if (fine && inv > 0.0f) {
-                if constexpr (FMT == EP_FP8_E4M3) w = e4m3_payload<DT>(v[k], inv);
-                else w = int8_payload<DT>(v[k], s, inv);
-            }
-            if (c.head_dim % 8 == 0) {  // 8-byte aligned: the pool is, and so is every row
-                *reinterpret_cast<uint2*>(data + at) = w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (at + j < c.head_dim) data[at + j] = uint8_t((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
-            }
-        }
+// Scale and reciprocal of an 8-bit row from the bits of its largest element: payload = v * inv, rounded;
+// inv = 0 where the payload is zeros.
+template <int DT, int FMT>
+__device__ __forceinline__ void row_scale(uint32_t bits, float& s, float& inv) {
+    const bool fine = bits < AbsBits<DT>::kInf;
+    const float amax = abs_value<DT>(bits);
+    if constexpr (FMT == EP_FP8_E4M3) {
+        const int e = e4m3_row_exponent(amax);
+        s = pow2f(e);
+        inv = pow2f(-e);
     } else {
-        constexpr bool NV = FMT == EP_NVFP4;
-#pragma unroll
-        for (int k = 0; k < NC; ++k) {
-            const int chunk = lane + k * LANES, at = 8 * chunk;
-            const Block b = block_scale<DT, NV>(lanes_max<NV ? 2 : 4>(abs_max8<DT>(v[k])), 1.0f, 1.0f);
-            const uint32_t codes = quantize8<DT, NV>(v[k], b);
-            if (!live || at / 2 >= int(c.row_bytes)) continue;
-            *reinterpret_cast<uint32_t*>(data + at / 2) = codes;
-            if (chunk % (NV ? 2 : 4) == 0 && at < c.head_dim) scales[chunk / (NV ? 2 : 4)] = uint8_t(b.byte);
-        }
+        s = amax >= 0x1p-100f ? __fmul_rn(amax, 1.0f / 127.0f) : 0.0f;
+        inv = s > 0.0f ? reciprocal_near(s) : 0.0f;
     }
+    if (!fine) s = __int_as_float(0x7fc00000), inv = 0.0f;
+}
+template <int DT, int FMT>
+__device__ __forceinline__ uint2 payload8(const Raw8<DT>& v, float s, float inv) {
+    if (inv == 0.0f) return make_uint2(0, 0);
+    if constexpr (FMT == EP_FP8_E4M3) return e4m3_payload<DT>(v, inv);
+    else return int8_payload<DT>(v, s, inv);
 }
 
-// A block takes a few tokens, all heads, of every cache (or of one, blockIdx.y, where there are few
-// tokens).  First it looks through the later tokens of the launch for its own slots: a token whose slot
-// is named again later is dropped, so that payload and scale of a slot always come from one token
-// (launches of one call follow each other, the later wins).  Rows then go in batches of LANES lanes a
-// row, whose loads are all on their way before the first is used.
-template <int DT, int FMT, int LANES, int NC>
-__global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) cache_write_kernel(const __grid_constant__ WriteArgs a) {
-    using T = typename Elem<DT>::T;
-    constexpr int kBatch = NC == 1 && DT != EP_F32 ? 4 : NC == 1 ? 2 : 1;
-    constexpr int kStep = kThreads / LANES;
-    __shared__ int64_t slot[kMaxWriteTokens];
-    __shared__ int dropped[kMaxWriteTokens];
-    wait_for_stream();
-    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
-    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
+// Where a block's tokens go: a token's slot, or -1 for one that is skipped.  A token whose slot a later
+// token of the launch names again is dropped, so that payload and scale of a slot always come from one
+// token (launches of one call follow each other, the later wins).  All threads; ends with a barrier.
+__device__ __forceinline__ void find_slots(const WriteArgs& a, int64_t t0, int n, int64_t* slot, int* dropped) {
     if (int(threadIdx.x) < n) {
         const int64_t s = a.slots[t0 + threadIdx.x];
         slot[threadIdx.x] = s >= 0 && s < a.n_slots ? s : -1;
@@ -197,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) cache_write_kernel(
     int64_t lo = a.n_slots, hi = -1;
     for (int i = 0; i < n; ++i)
         if (slot[i] >= 0) lo = min(lo, slot[i]), hi = max(hi, slot[i]);
+    const uint64_t span = uint64_t(hi - lo);
     if (hi >= 0)
         for (int64_t j0 = t0 + 1 + threadIdx.x; j0 < a.tokens; j0 += 4 * kThreads) {
             int64_t s[4];
@@ -204,39 +169,145 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) cache_write_kernel(
             for (int u = 0; u < 4; ++u) s[u] = j0 + u * kThreads < a.tokens ? a.slots[j0 + u * kThreads] : -1;
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (s[u] >= lo && s[u] <= hi)
+                if (uint64_t(s[u] - lo) <= span)
                     for (int i = 0; i < n; ++i)
                         if (slot[i] == s[u] && t0 + i < j0 + u * kThreads) dropped[i] = 1;
         }
     __syncthreads();
     if (int(threadIdx.x) < n && dropped[threadIdx.x]) slot[threadIdx.x] = -1;
     __syncthreads();
+}
 
-    const int rows = n * a.heads, lane = threadIdx.x % LANES;
-    for (int ci = blockIdx.y; ci < a.n; ci += gridDim.y) {
-        const CacheView& c = a.c[ci];
-        const T* src = static_cast<const T*>(c.heads) + t0 * c.token_stride;
-        // every lane of a warp stays in the loop: rows past the end are zeros and not written
-        for (int base = 0; base < rows; base += kBatch * kStep) {
-            Raw8<DT> v[kBatch][NC];
-            int64_t row[kBatch];
+// A block takes a few tokens, all heads of all caches; rows go in batches of LANES lanes a row, whose loads
+// are all on their way before the first is used, those of the first batch before the slots are looked up.
+template <int DT, int FMT, int LANES>
+__global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_kernel(const __grid_constant__ WriteArgs a) {
+    using T = typename Elem<DT>::T;
+    constexpr int kBatch = DT == EP_F32 ? 2 : 4, kStep = kThreads / LANES;
+    constexpr bool kFp4 = FMT == EP_MXFP4 || FMT == EP_NVFP4;
+    __shared__ int64_t slot[kMaxWriteTokens];
+    __shared__ int dropped[kMaxWriteTokens];
+    wait_for_stream();
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
+    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
+    const int rows = n * a.heads, all = a.n * rows;
+    const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES, e = 16 * lane;
+    Raw8<DT> v[kBatch][2];
+    auto load = [&](int base) {
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int r = base + u * kStep + int(threadIdx.x) / LANES;
-                const int i = min(quotient(r, a.heads_inv), n - 1), h = r - i * a.heads;
-                row[u] = r < rows && slot[i] >= 0 ? slot[i] * a.heads + h : -1;
-                const T* p = src + i * c.token_stride + h * c.head_stride;
+        for (int u = 0; u < kBatch; ++u) {
+            int r = base + u * kStep + sub;
+            const int ci = r >= rows ? 1 : 0;
+            r -= ci ? rows : 0;
+            const int i = quotient(r, a.heads_inv), h = r - i * a.heads;
+            const CacheView& c = a.c[ci];
+            const bool in = base + u * kStep + sub < all;
+            const T* p = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride + e;
+            v[u][0] = load_raw8<DT>(p, in && e < c.head_dim ? 8 : 0, 16);
+            v[u][1] = load_raw8<DT>(p + 8, in && e + 8 < c.head_dim ? 8 : 0, 16);
+        }
+    };
+    load(0);
+    find_slots(a, t0, n, slot, dropped);
+    // every lane of a warp stays in the loop: rows past the end are zeros and not written
+    for (int base = 0;;) {
 #pragma unroll
-                for (int k = 0; k < NC; ++k) {
-                    const int e = 8 * (lane + k * LANES);
-                    v[u][k] = load_raw8<DT>(p + e, row[u] >= 0 ? min(8, c.head_dim - e) : 0, c.width);
+        for (int u = 0; u < kBatch; ++u) {
+            if (base + u * kStep >= all) break;
+            int r = base + u * kStep + sub;
+            const bool in = r < all;
+            const int ci = r >= rows ? 1 : 0;
+            r -= ci ? rows : 0;
+            const int i = in ? quotient(r, a.heads_inv) : 0, h = r - i * a.heads;
+            const CacheView& c = a.c[ci];
+            const int64_t to = in ? slot[i] : -1, row = to * a.heads + h;
+            const bool live = to >= 0 && e < c.head_dim, both_live = e + 8 < c.head_dim;
+            uint32_t bits = max(abs_max8<DT>(v[u][0]), abs_max8<DT>(v[u][1]));
+            if constexpr (kFp4) {
+                constexpr bool NV = FMT == EP_NVFP4;
+                const Block b = block_scale<DT, NV>(lanes_max<NV ? 1 : 2>(bits), 1.0f, 1.0f);
+                const uint2 w = make_uint2(quantize8<DT, NV>(v[u][0], b), quantize8<DT, NV>(v[u][1], b));
+                // the lane past an odd number of sixteens writes the row's padding
+                if (to >= 0 && 8 * lane < int(c.row_bytes)) {
+                    *reinterpret_cast<uint2*>(c.data + row * c.row_bytes + 8 * lane) = w;
+                    if (live && (NV || lane % 2 == 0)) c.scales[row * c.scale_bytes + (NV ? lane : lane / 2)] = uint8_t(b.byte);
+                }
+            } else {
+                bits = lanes_max<LANES>(bits);
+                float s, inv;
+                row_scale<DT, FMT>(bits, s, inv);
+                if (live) {
+                    uint8_t* to8 = c.data + row * c.row_bytes + e;
+                    const uint2 w0 = payload8<DT, FMT>(v[u][0], s, inv), w1 = payload8<DT, FMT>(v[u][1], s, inv);
+                    if (c.head_dim % 16 == 0) {
+                        *reinterpret_cast<uint4*>(to8) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                    } else {
+                        *reinterpret_cast<uint2*>(to8) = w0;
+                        if (both_live) *reinterpret_cast<uint2*>(to8 + 8) = w1;
+                    }
+                    if (lane == 0) reinterpret_cast<float*>(c.scales)[row] = s;
                 }
             }
+        }
+        base += kBatch * kStep;
+        if (base >= all) break;
+        load(base);
+    }
+}
+
+// The same for any head: a warp a row, 4 chunks of 8 elements a lane, at any alignment.
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kThreads) cache_write_any_kernel(const __grid_constant__ WriteArgs a) {
+    using T = typename Elem<DT>::T;
+    constexpr int NC = kMaxHeadDim / 256;
+    __shared__ int64_t slot[kMaxWriteTokens];
+    __shared__ int dropped[kMaxWriteTokens];
+    wait_for_stream();
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
+    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
+    find_slots(a, t0, n, slot, dropped);
+    const int rows = n * a.heads, lane = threadIdx.x % 32;
+    for (int r = threadIdx.x / 32; r < a.n * rows; r += kThreads / 32) {
+        const int ci = r >= rows, i = quotient(r - ci * rows, a.heads_inv), h = r - ci * rows - i * a.heads;
+        const CacheView& c = a.c[ci];
+        const int64_t to = slot[i], row = to * a.heads + h;
+        if (to < 0) continue;
+        const T* src = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride;
+        uint8_t* data = c.data + row * c.row_bytes;
+        Raw8<DT> v[NC];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                if (base + u * kStep >= rows) break;
-                write_row<DT, FMT, LANES, NC>(c, c.data + row[u] * c.row_bytes, c.scales + row[u] * c.scale_bytes, lane, v[u],
-                                              row[u] >= 0);
+        for (int k = 0; k < NC; ++k) v[k] = load_raw8<DT>(src + 8 * (lane + 32 * k), min(8, c.head_dim - 8 * (lane + 32 * k)), c.width);
+        if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) bits = max(bits, abs_max8<DT>(v[k]));
+            float s, inv;
+            row_scale<DT, FMT>(lanes_max<32>(bits), s, inv);
+            if (lane == 0) reinterpret_cast<float*>(c.scales)[row] = s;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                const int at = 8 * (lane + 32 * k);
+                if (at >= c.head_dim) break;
+                const uint2 w = payload8<DT, FMT>(v[k], s, inv);
+                if (c.head_dim % 8 == 0) {
+                    *reinterpret_cast<uint2*>(data + at) = w;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (at + j < c.head_dim) data[at + j] = uint8_t((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
+                }
+            }
+        } else {
+            constexpr bool NV = FMT == EP_NVFP4;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+                const int chunk = lane + 32 * k;
+                const Block b = block_scale<DT, NV>(lanes_max<NV ? 2 : 4>(abs_max8<DT>(v[k])), 1.0f, 1.0f);
+                const uint32_t codes = quantize8<DT, NV>(v[k], b);
+                if (4 * chunk >= int(c.row_bytes)) continue;
+                *reinterpret_cast<uint32_t*>(data + 4 * chunk) = codes;
+                if (chunk % (NV ? 2 : 4) == 0 && 8 * chunk < c.head_dim)
+                    c.scales[row * c.scale_bytes + chunk / (NV ? 2 : 4)] = uint8_t(b.byte);
             }
         }
     }
@@ -244,53 +315,23 @@ __global__ void __launch_bounds__(kThreads, NC == 1 ? 4 : 2) cache_write_kernel(
 
 // ---- reading -----------------------------------------------------------------------------------
 
-// A chunk of 8 elements as it lies in the cache, and its scale.
+// The values of 8 payload elements: two words, or one of the 4-bit formats.
 template <int FMT>
-struct Chunk {
-    uint2 w;
-    float s;
-};
-template <int FMT>
-__device__ __forceinline__ Chunk<FMT> load_chunk(const CacheView& c, int64_t row, int chunk) {
-    Chunk<FMT> q;
-    q.w = make_uint2(0, 0);
-    q.s = 0.0f;
-    if (row < 0) return q;  // no such page
-    const uint8_t* data = c.data + row * c.row_bytes;
-    const uint8_t* scales = c.scales + row * c.scale_bytes;
-    if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
-        const int at = 8 * chunk;
-        if (c.head_dim % 8 == 0) {
-            q.w = *reinterpret_cast<const uint2*>(data + at);
-        } else {
-            uint32_t w[2] = {0, 0};
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (at + j < c.head_dim) w[j / 4] |= uint32_t(data[at + j]) << (8 * (j % 4));
-            q.w = make_uint2(w[0], w[1]);
-        }
-        q.s = *reinterpret_cast<const float*>(scales);
-    } else {
-        q.w.x = *reinterpret_cast<const uint32_t*>(data + 4 * chunk);
-        q.s = scale_value<FMT == EP_NVFP4>(scales[chunk / (FMT == EP_NVFP4 ? 2 : 4)]);
-    }
-    return q;
-}
-template <int FMT>
-__device__ __forceinline__ void chunk_values(const Chunk<FMT>& q, float* v) {
+__device__ __forceinline__ void values8(uint32_t lo, uint32_t hi, float s, float* v) {
     if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t two = ((j < 2 ? q.w.x : q.w.y) >> (16 * (j % 2))) & 0xffffu;
+            const uint32_t two = ((j < 2 ? lo : hi) >> (16 * (j % 2))) & 0xffffu;
             const float2 f = FMT == EP_FP8_E4M3 ? e4m3x2_value(two)
                                                 : make_float2(float(int8_t(two & 0xff)), float(int8_t(two >> 8)));
-            v[2 * j] = f.x * q.s;
-            v[2 * j + 1] = f.y * q.s;
+            const float2 p = mul2(f, both(s));
+            v[2 * j] = p.x;
+            v[2 * j + 1] = p.y;
         }
     } else {
-        e2m1_values8(q.w.x, v);
+        e2m1_values8(lo, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= q.s;
+        for (int j = 0; j < 8; ++j) v[j] *= s;
     }
 }
 
@@ -305,29 +346,21 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int n_seqs, int64_
     return lo;
 }
 
-// A block takes up to 64 tokens, all heads, of every output (or of one, blockIdx.y, where there are few
-// tokens): finds their slots, then reads rows of LANES lanes in batches, whose loads are all on their way
-// before the first is used.
-template <int DT, int FMT, int LANES>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
-    using T = typename Elem<DT>::T;
-    constexpr int kBatch = 4, kStep = kThreads / LANES;
-    __shared__ int32_t starts[kSharedSeqs + 1];
-    __shared__ int64_t slot[kMaxReadTokens];  // -1: zeros, -2: past the sequences
-    wait_for_stream();
-    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
-    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
+// The slots of a block's tokens: -1 for one without a valid page (zeros), -2 past the sequences.  All
+// threads; ends with a barrier.
+__device__ __forceinline__ void find_pages(const ReadArgs& a, int64_t t0, int n, int32_t* starts, int64_t* slot) {
     const bool shared = a.n_seqs <= kSharedSeqs;
-    if (shared)
+    if (shared) {
         for (int i = threadIdx.x; i <= a.n_seqs; i += kThreads) starts[i] = a.cu_seqlens[i];
-    __syncthreads();
+        __syncthreads();
+    }
     if (int(threadIdx.x) < n) {
         const int32_t* cu = shared ? starts : a.cu_seqlens;
         const int64_t t = t0 + threadIdx.x;
         int64_t s = -2;
         const int seq = sequence_of(cu, a.n_seqs, t);
         const int64_t pos = t - cu[seq];
-        if (pos >= 0 && t < cu[seq + 1]) {  // both differences fit 32 bits: tokens do
+        if (pos >= 0 && t < cu[seq + 1]) {  // the position fits 32 bits: tokens do
             s = -1;
             const uint32_t p = uint32_t(pos) / uint32_t(a.page_size);
             if (int64_t(p) < a.pages_per_seq) {
@@ -338,69 +371,158 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
         slot[threadIdx.x] = s;
     }
     __syncthreads();
-    const int rows = n * a.heads;
-    for (int ci = blockIdx.y; ci < a.n; ci += gridDim.y) {
-        const CacheView& c = a.c[ci];
-        T* out = static_cast<T*>(c.heads) + t0 * c.token_stride;
-        const int chunks = (c.head_dim + 7) / 8;
-        for (int chunk = threadIdx.x % LANES; chunk < chunks; chunk += LANES)
-            for (int base = int(threadIdx.x) / LANES; base < rows; base += kBatch * kStep) {
-                Chunk<FMT> q[kBatch];
-                T* dst[kBatch];
+}
+
+// A block takes up to 64 tokens, all heads of all outputs: finds their slots, then reads rows of LANES
+// lanes in batches, whose loads are all on their way before the first is used.
+template <int DT, int FMT, int LANES>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
+    using T = typename Elem<DT>::T;
+    constexpr int kBatch = 4, kStep = kThreads / LANES;
+    constexpr bool kFp4 = FMT == EP_MXFP4 || FMT == EP_NVFP4;
+    __shared__ int32_t starts[kSharedSeqs + 1];
+    __shared__ int64_t slot[kMaxReadTokens];
+    wait_for_stream();
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
+    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
+    find_pages(a, t0, n, starts, slot);
+    const int rows = n * a.heads, all = a.n * rows, lane = threadIdx.x % LANES, e = 16 * lane;
+    for (int base = threadIdx.x / LANES; base < all; base += kBatch * kStep) {
+        uint4 q[kBatch];
+        float s[kBatch];
+        T* dst[kBatch];
+        bool second[kBatch];
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int r = base + u * kStep;
-                    const int t = min(quotient(r, a.heads_inv), n - 1), h = r - t * a.heads;
-                    const int64_t s = slot[t];
-                    dst[u] = r < rows && s != -2 ? out + t * c.token_stride + h * c.head_stride + 8 * chunk : nullptr;
-                    q[u] = load_chunk<FMT>(c, r < rows && s >= 0 ? s * a.heads + h : -1, chunk);
-                }
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    if (!dst[u]) continue;
-                    float v[8];
-                    chunk_values<FMT>(q[u], v);
-                    store8<DT>(dst[u], min(8, c.head_dim - 8 * chunk), c.width, v);
+        for (int u = 0; u < kBatch; ++u) {
+            int r = base + u * kStep;
+            const bool in = r < all;
+            const int ci = r >= rows && in ? 1 : 0;
+            r = in ? r - (ci ? rows : 0) : 0;
+            const int t = quotient(r, a.heads_inv), h = r - t * a.heads;
+            const CacheView& c = a.c[ci];
+            const int64_t from = slot[t], row = from * a.heads + h;
+            dst[u] = in && from != -2 && e < c.head_dim ? static_cast<T*>(c.heads) + (t0 + t) * c.token_stride + h * c.head_stride + e : nullptr;
+            second[u] = e + 8 < c.head_dim;
+            q[u] = make_uint4(0, 0, 0, 0);
+            s[u] = 0.0f;
+            if (dst[u] && from >= 0) {
+                if constexpr (kFp4) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(c.data + row * c.row_bytes + 8 * lane);
+                    q[u].x = w.x;
+                    q[u].z = w.y;
+                    s[u] = scale_value<FMT == EP_NVFP4>(c.scales[row * c.scale_bytes + (FMT == EP_NVFP4 ? lane : lane / 2)]);
+                } else {
+                    const uint8_t* p = c.data + row * c.row_bytes + e;
+                    if (c.head_dim % 16 == 0) {
+                        q[u] = *reinterpret_cast<const uint4*>(p);
+                    } else {
+                        const uint2 w0 = *reinterpret_cast<const uint2*>(p);
+                        q[u].x = w0.x, q[u].y = w0.y;
+                        if (second[u]) {
+                            const uint2 w1 = *reinterpret_cast<const uint2*>(p + 8);
+                            q[u].z = w1.x, q[u].w = w1.y;
+                        }
+                    }
+                    s[u] = reinterpret_cast<const float*>(c.scales)[row];
                 }
             }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (!dst[u]) continue;
+            float v[8];
+            values8<FMT>(q[u].x, q[u].y, s[u], v);
+            store8<DT>(dst[u], 8, 16, v);
+            if (second[u]) {
+                values8<FMT>(q[u].z, q[u].w, s[u], v);
+                store8<DT>(dst[u] + 8, 8, 16, v);
+            }
+        }
+    }
+}
+
+// The same for any head: a warp a row, 8 elements a lane, at any alignment.
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kThreads) cache_read_any_kernel(const __grid_constant__ ReadArgs a) {
+    using T = typename Elem<DT>::T;
+    __shared__ int32_t starts[kSharedSeqs + 1];
+    __shared__ int64_t slot[kMaxReadTokens];
+    wait_for_stream();
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
+    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
+    find_pages(a, t0, n, starts, slot);
+    const int rows = n * a.heads, lane = threadIdx.x % 32;
+    for (int r = threadIdx.x / 32; r < a.n * rows; r += kThreads / 32) {
+        const int ci = r >= rows, t = quotient(r - ci * rows, a.heads_inv), h = r - ci * rows - t * a.heads;
+        const CacheView& c = a.c[ci];
+        const int64_t from = slot[t], row = from * a.heads + h;
+        if (from == -2) continue;
+        T* dst = static_cast<T*>(c.heads) + (t0 + t) * c.token_stride + h * c.head_stride;
+        const uint8_t* data = c.data + row * c.row_bytes;
+        for (int e = 8 * lane; e < c.head_dim; e += 256) {
+            const int m = min(8, c.head_dim - e);
+            uint32_t w[2] = {0, 0};
+            float s = 0.0f, v[8];
+            if (from >= 0) {
+                if constexpr (FMT == EP_MXFP4 || FMT == EP_NVFP4) {
+                    w[0] = *reinterpret_cast<const uint32_t*>(data + e / 2);
+                    s = scale_value<FMT == EP_NVFP4>(c.scales[row * c.scale_bytes + e / (FMT == EP_NVFP4 ? 16 : 32)]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < m) w[j / 4] |= uint32_t(data[e + j]) << (8 * (j % 4));
+                    s = reinterpret_cast<const float*>(c.scales)[row];
+                }
+            }
+            values8<FMT>(w[0], w[1], s, v);
+            store8<DT>(dst + e, m, c.width, v);
+        }
     }
 }
 
 // ---- host side -----------------------------------------------------------------------------------
-// Lanes of a row: a power of two of at least 4 (a block of 32 elements), 8 elements each.
-int lanes_of(int head_dim) { return head_dim <= 64 ? 8 : head_dim <= 128 ? 16 : 32; }
+// What serves a call: the lanes of a row at 16 elements each, or 0 for any head.
+int lanes_of(const CacheView* c, int n) {
+    int dim = 0;
+    for (int i = 0; i < n; ++i) {
+        if (c[i].head_dim % 8 != 0 || c[i].head_dim > kMaxFastDim || c[i].width != 16) return 0;
+        dim = std::max(dim, c[i].head_dim);
+    }
+    return dim <= 64 ? 4 : dim <= 128 ? 8 : 16;
+}
 
 template <int DT, int FMT>
-cudaError_t launch_write(const WriteArgs& w, int head_dim, dim3 grid, cudaStream_t st) {
-    const auto kernel = head_dim > 256            ? cache_write_kernel<DT, FMT, 32, 4>
-                        : lanes_of(head_dim) == 32 ? cache_write_kernel<DT, FMT, 32, 1>
-                        : lanes_of(head_dim) == 16 ? cache_write_kernel<DT, FMT, 16, 1>
-                                                   : cache_write_kernel<DT, FMT, 8, 1>;
+cudaError_t launch_write(const WriteArgs& w, int lanes, dim3 grid, cudaStream_t st) {
+    const auto kernel = lanes == 4   ? cache_write_kernel<DT, FMT, 4>
+                        : lanes == 8 ? cache_write_kernel<DT, FMT, 8>
+                        : lanes == 16 ? cache_write_kernel<DT, FMT, 16>
+                                      : cache_write_any_kernel<DT, FMT>;
     return op::launch(kernel, grid, dim3(kThreads), 0, st, w);
 }
 template <int DT>
-cudaError_t write_as(int fmt, const WriteArgs& w, int head_dim, dim3 grid, cudaStream_t st) {
+cudaError_t write_as(int fmt, const WriteArgs& w, int lanes, dim3 grid, cudaStream_t st) {
     switch (fmt) {
-        case EP_FP8_E4M3: return launch_write<DT, EP_FP8_E4M3>(w, head_dim, grid, st);
-        case EP_INT8: return launch_write<DT, EP_INT8>(w, head_dim, grid, st);
-        case EP_MXFP4: return launch_write<DT, EP_MXFP4>(w, head_dim, grid, st);
-        default: return launch_write<DT, EP_NVFP4>(w, head_dim, grid, st);
+        case EP_FP8_E4M3: return launch_write<DT, EP_FP8_E4M3>(w, lanes, grid, st);
+        case EP_INT8: return launch_write<DT, EP_INT8>(w, lanes, grid, st);
+        case EP_MXFP4: return launch_write<DT, EP_MXFP4>(w, lanes, grid, st);
+        default: return launch_write<DT, EP_NVFP4>(w, lanes, grid, st);
     }
 }
 template <int DT, int FMT>
-cudaError_t launch_read(const ReadArgs& r, int head_dim, dim3 grid, cudaStream_t st) {
-    const auto kernel = lanes_of(head_dim) == 32   ? cache_read_kernel<DT, FMT, 32>
-                        : lanes_of(head_dim) == 16 ? cache_read_kernel<DT, FMT, 16>
-                                                   : cache_read_kernel<DT, FMT, 8>;
+cudaError_t launch_read(const ReadArgs& r, int lanes, dim3 grid, cudaStream_t st) {
+    const auto kernel = lanes == 4   ? cache_read_kernel<DT, FMT, 4>
+                        : lanes == 8 ? cache_read_kernel<DT, FMT, 8>
+                        : lanes == 16 ? cache_read_kernel<DT, FMT, 16>
+                                      : cache_read_any_kernel<DT, FMT>;
     return op::launch(kernel, grid, dim3(kThreads), 0, st, r);
 }
 template <int DT>
-cudaError_t read_as(int fmt, const ReadArgs& r, int head_dim, dim3 grid, cudaStream_t st) {
+cudaError_t read_as(int fmt, const ReadArgs& r, int lanes, dim3 grid, cudaStream_t st) {
     switch (fmt) {
-        case EP_FP8_E4M3: return launch_read<DT, EP_FP8_E4M3>(r, head_dim, grid, st);
-        case EP_INT8: return launch_read<DT, EP_INT8>(r, head_dim, grid, st);
-        case EP_MXFP4: return launch_read<DT, EP_MXFP4>(r, head_dim, grid, st);
-        default: return launch_read<DT, EP_NVFP4>(r, head_dim, grid, st);
+        case EP_FP8_E4M3: return launch_read<DT, EP_FP8_E4M3>(r, lanes, grid, st);
+        case EP_INT8: return launch_read<DT, EP_INT8>(r, lanes, grid, st);
+        case EP_MXFP4: return launch_read<DT, EP_MXFP4>(r, lanes, grid, st);
+        default: return launch_read<DT, EP_NVFP4>(r, lanes, grid, st);
     }
 }
 
@@ -469,7 +591,7 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
     if (tokens > 0 && (!slots || !op::aligned(slots, 8))) return set_error(EP_ERR_ARG, "ep_cache_write: slots are NULL or misaligned");
     rc = device_of(caches, src, n, "ep_cache_write", sms);
     if (rc != EP_OK || tokens == 0 || caches[0].n_pages == 0) return rc;
-    const int dim = std::max(src[0].head_dim, src[n - 1].head_dim);
+    const int lanes = lanes_of(w.c, n);
     const int es = op::elem_bytes(src[0].dtype);
     w.n_slots = caches[0].n_pages * caches[0].page_size;
     w.n = n;
@@ -482,12 +604,12 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
         part.tokens = std::min<int64_t>(kLaunchTokens, tokens - t0);
         for (int i = 0; i < n; ++i)
             part.c[i].heads = static_cast<uint8_t*>(w.c[i].heads) + t0 * w.c[i].token_stride * es;
-        // few tokens are spread over the SMs, keys and values apart
+        // few tokens are spread over the SMs
         part.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxWriteTokens, part.tokens / (2 * sms))));
-        const dim3 grid(unsigned(op::div_up(part.tokens, part.per_block)), part.per_block < kMaxWriteTokens ? unsigned(n) : 1u);
-        const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, dim, grid, st)
-                              : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, dim, grid, st)
-                                                        : write_as<EP_F32>(caches[0].format, part, dim, grid, st);
+        const dim3 grid(unsigned(op::div_up(part.tokens, part.per_block)));
+        const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, lanes, grid, st)
+                              : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, lanes, grid, st)
+                                                        : write_as<EP_F32>(caches[0].format, part, lanes, grid, st);
         if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_cache_write: ") + cudaGetErrorString(e));
     }
     return EP_OK;
@@ -518,14 +640,14 @@ extern "C" int ep_cache_read(const ep_cache* caches, const ep_heads* out, int n,
     r.heads = caches[0].heads;
     r.heads_inv = 1.0f / float(r.heads);
     r.n = n;
-    // few tokens are spread over the SMs, keys and values apart
+    // few tokens are spread over the SMs
     r.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxReadTokens, r.tokens / (4 * sms))));
-    const dim3 grid(unsigned(op::div_up(r.tokens, r.per_block)), r.per_block < kMaxReadTokens ? unsigned(n) : 1u);
-    const int dim = std::max(out[0].head_dim, out[n - 1].head_dim);
+    const dim3 grid(unsigned(op::div_up(r.tokens, r.per_block)));
+    const int lanes = lanes_of(r.c, n);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = out[0].dtype == EP_BF16   ? read_as<EP_BF16>(caches[0].format, r, dim, grid, st)
-                          : out[0].dtype == EP_FP16 ? read_as<EP_FP16>(caches[0].format, r, dim, grid, st)
-                                                    : read_as<EP_F32>(caches[0].format, r, dim, grid, st);
+    const cudaError_t e = out[0].dtype == EP_BF16   ? read_as<EP_BF16>(caches[0].format, r, lanes, grid, st)
+                          : out[0].dtype == EP_FP16 ? read_as<EP_FP16>(caches[0].format, r, lanes, grid, st)
+                                                    : read_as<EP_F32>(caches[0].format, r, lanes, grid, st);
     if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_cache_read: ") + cudaGetErrorString(e));
     return EP_OK;
 }

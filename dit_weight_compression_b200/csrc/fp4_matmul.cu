@@ -121,6 +121,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
             bar_init(empty(s), 1);
         }
         bar_init(done, 1);
+        prefetch_map(&b_map);
+        prefetch_map(&a_map);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tmem_alloc(slot, G::kColumns);
@@ -334,6 +336,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
         }
         bar_init(summed, 1);
         bar_init(taken, 16);  // the 8 reading warps of both CTAs
+        prefetch_map(&a_map);
+        prefetch_map(&b_map);
+        prefetch_map(&as_map);
+        prefetch_map(&bs_map);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tmem_alloc_pair(slot, 512);
@@ -504,14 +510,31 @@ bool operand_map(CUtensorMap* map, const ep_fp4_tensor* t, int box_rows) {
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Sets the shared memory size of a variant's kernel, once per device.
+// Clusters of `split` CTAs of a variant that fit the device at one time (looked up once), after setting
+// its kernel's shared memory.
+constexpr int kMaxSplit = 8;
 template <int NT, bool NV>
-cudaError_t allow_smem(int dev) {
-    static std::atomic<bool> done[kMaxDevices];
-    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(fp4_split_kernel<NT, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(Geo<NT, NV>::kSmem));
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+cudaError_t clusters_of(int dev, int split, int& clusters) {
+    static std::atomic<int> known[kMaxDevices][kMaxSplit + 1];
+    clusters = known[dev][split].load(std::memory_order_relaxed);
+    if (clusters > 0) return cudaSuccess;
+    const auto kernel = fp4_split_kernel<NT, NV>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Geo<NT, NV>::kSmem));
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(split));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Geo<NT, NV>::kSmem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = unsigned(split);
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+    }
+    if (e == cudaSuccess && clusters < 1) e = cudaErrorInvalidConfiguration;
+    if (e == cudaSuccess) known[dev][split].store(clusters, std::memory_order_relaxed);
     return e;
 }
 
@@ -569,16 +592,22 @@ int run_pairs(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& 
 }
 
 template <int NT, bool NV>
-int run_split(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int sms, int dev, cudaStream_t st) {
+int run_split(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int dev, cudaStream_t st) {
     using G = Geo<NT, NV>;
     CUtensorMap b_map, a_map;
     if (!operand_map(&b_map, b, 128) || !operand_map(&a_map, a, NT)) return set_error(EP_ERR_CUDA, "ep_fp4_matmul: tensor map");
-    // CTAs of one tile: as many as fill two CTAs an SM, at most 8 and one stage each
+    // CTAs of one tile: the most whose clusters all fit the device at once, with four stages each.  (4096
+    // outputs of 4096 for one token: 5.4 us with 4, 6.5 with 8 of two stages; 300 tokens: 11.1 us with 2,
+    // 16.7 with 3, which need a second round.)
     const int64_t tiles = int64_t(args.n_tiles) * op::div_up(a->rows, NT);
-    const int split = int(std::max<int64_t>(1, std::min<int64_t>({8, args.steps, 2 * int64_t(sms) / tiles})));
+    int split = std::min(kMaxSplit, (args.steps + 3) / 4), clusters = 0;
+    cudaError_t e = clusters_of<NT, NV>(dev, 1, clusters);
+    for (; e == cudaSuccess && split > 1; --split) {
+        e = clusters_of<NT, NV>(dev, split, clusters);
+        if (tiles <= clusters) break;
+    }
     const int64_t grid = tiles * split;
     if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: too many tiles");
-    cudaError_t e = allow_smem<NT, NV>(dev);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(grid));
@@ -600,13 +629,15 @@ int run_split(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& 
 }
 
 template <bool NV>
-int matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int sms, int dev, cudaStream_t st) {
+int matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int dev, cudaStream_t st) {
     const int64_t m = a->rows;
-    if (m <= 16) return run_split<16, NV>(a, b, args, sms, dev, st);
-    if (m <= 32) return run_split<32, NV>(a, b, args, sms, dev, st);
-    if (m <= 64) return run_split<64, NV>(a, b, args, sms, dev, st);
-    if (op::div_up(m, 128) * op::div_up(b->rows, 256) >= sms) return run_pairs<NV>(a, b, args, dev, st);
-    return run_split<128, NV>(a, b, args, sms, dev, st);
+    if (m <= 16) return run_split<16, NV>(a, b, args, dev, st);
+    if (m <= 32) return run_split<32, NV>(a, b, args, dev, st);
+    if (m <= 64) return run_split<64, NV>(a, b, args, dev, st);
+    if (m <= 128) return run_split<128, NV>(a, b, args, dev, st);
+    // (130 tokens, 8192 outputs of 28672: 41 us in pairs, 51 split; 300, 4096 of 4096: 10.8 and 12.3; only
+    // where 256 tokens meet fewer outputs than 4096 split is ahead, 9.2 against 10.4.)
+    return run_pairs<NV>(a, b, args, dev, st);
 }
 
 }  // namespace
@@ -659,7 +690,7 @@ extern "C" int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, con
         if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_matmul: ") + cudaGetErrorString(e));
         return EP_OK;
     }
-    return a->format == EP_NVFP4 ? matmul<true>(a, b, args, sms, dev, st) : matmul<false>(a, b, args, sms, dev, st);
+    return a->format == EP_NVFP4 ? matmul<true>(a, b, args, dev, st) : matmul<false>(a, b, args, dev, st);
 }
 
 extern "C" int ep_op_status(void* stream) {

@@ -29,8 +29,11 @@ namespace ms {
 
 constexpr uint32_t kFullMask = 0xffffffffu;
 
-// A dependent launch's first step: everything before this kernel in its stream has finished.
-__device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A dependent launch's first step: everything before this kernel in its stream has finished, and the next
+// kernel may be set up from here on (it waits in the same way before it touches memory).
+__device__ __forceinline__ void wait_for_stream() {
+    asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 template <int DT>
 struct Elem;
