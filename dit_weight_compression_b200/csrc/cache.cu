@@ -191,7 +191,9 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
     const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
     const int n = int(min(int64_t(a.per_block), a.tokens - t0));
     const int rows = n * a.heads, all = a.n * rows;
-    const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES, e = 16 * lane;
+    const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    // 4-bit: sixteen neighbours, of one block; 8-bit: twice eight, so that lanes touch neighbouring bytes
+    const int e = (kFp4 ? 16 : 8) * lane, e2 = e + (kFp4 ? 8 : 8 * LANES);
     Raw8<DT> v[kBatch][2];
     auto load = [&](int base) {
 #pragma unroll
@@ -202,9 +204,9 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
             const int i = quotient(r, a.heads_inv), h = r - i * a.heads;
             const CacheView& c = a.c[ci];
             const bool in = base + u * kStep + sub < all;
-            const T* p = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride + e;
-            v[u][0] = load_raw8<DT>(p, in && e < c.head_dim ? 8 : 0, 16);
-            v[u][1] = load_raw8<DT>(p + 8, in && e + 8 < c.head_dim ? 8 : 0, 16);
+            const T* p = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride;
+            v[u][0] = load_raw8<DT>(p + e, in && e < c.head_dim ? 8 : 0, 16);
+            v[u][1] = load_raw8<DT>(p + e2, in && e2 < c.head_dim ? 8 : 0, 16);
         }
     };
     load(0);
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
             const int i = in ? quotient(r, a.heads_inv) : 0, h = r - i * a.heads;
             const CacheView& c = a.c[ci];
             const int64_t to = in ? slot[i] : -1, row = to * a.heads + h;
-            const bool live = to >= 0 && e < c.head_dim, both_live = e + 8 < c.head_dim;
+            const bool live = to >= 0 && e < c.head_dim;
             uint32_t bits = max(abs_max8<DT>(v[u][0]), abs_max8<DT>(v[u][1]));
             if constexpr (kFp4) {
                 constexpr bool NV = FMT == EP_NVFP4;
@@ -237,14 +239,9 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
                 float s, inv;
                 row_scale<DT, FMT>(bits, s, inv);
                 if (live) {
-                    uint8_t* to8 = c.data + row * c.row_bytes + e;
-                    const uint2 w0 = payload8<DT, FMT>(v[u][0], s, inv), w1 = payload8<DT, FMT>(v[u][1], s, inv);
-                    if (c.head_dim % 16 == 0) {
-                        *reinterpret_cast<uint4*>(to8) = make_uint4(w0.x, w0.y, w1.x, w1.y);
-                    } else {
-                        *reinterpret_cast<uint2*>(to8) = w0;
-                        if (both_live) *reinterpret_cast<uint2*>(to8 + 8) = w1;
-                    }
+                    uint8_t* data = c.data + row * c.row_bytes;
+                    *reinterpret_cast<uint2*>(data + e) = payload8<DT, FMT>(v[u][0], s, inv);
+                    if (e2 < c.head_dim) *reinterpret_cast<uint2*>(data + e2) = payload8<DT, FMT>(v[u][1], s, inv);
                     if (lane == 0) reinterpret_cast<float*>(c.scales)[row] = s;
                 }
             }
@@ -386,10 +383,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
     const int n = int(min(int64_t(a.per_block), a.tokens - t0));
     find_pages(a, t0, n, starts, slot);
-    const int rows = n * a.heads, all = a.n * rows, lane = threadIdx.x % LANES, e = 16 * lane;
+    const int rows = n * a.heads, all = a.n * rows, lane = threadIdx.x % LANES;
     for (int base = threadIdx.x / LANES; base < all; base += kBatch * kStep) {
-        uint4 q[kBatch];
-        float s[kBatch];
+        uint2 q[kBatch][2];  // chunks `lane` and `lane + LANES` of 8 elements
+        float s[kBatch][kFp4 ? 2 : 1];
         T* dst[kBatch];
         bool second[kBatch];
 #pragma unroll
@@ -401,29 +398,27 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
             const int t = quotient(r, a.heads_inv), h = r - t * a.heads;
             const CacheView& c = a.c[ci];
             const int64_t from = slot[t], row = from * a.heads + h;
-            dst[u] = in && from != -2 && e < c.head_dim ? static_cast<T*>(c.heads) + (t0 + t) * c.token_stride + h * c.head_stride + e : nullptr;
-            second[u] = e + 8 < c.head_dim;
-            q[u] = make_uint4(0, 0, 0, 0);
-            s[u] = 0.0f;
+            dst[u] = in && from != -2 && 8 * lane < c.head_dim
+                         ? static_cast<T*>(c.heads) + (t0 + t) * c.token_stride + h * c.head_stride + 8 * lane
+                         : nullptr;
+            second[u] = 8 * (lane + LANES) < c.head_dim;
+            q[u][0] = q[u][1] = make_uint2(0, 0);
+            s[u][0] = s[u][kFp4 ? 1 : 0] = 0.0f;
             if (dst[u] && from >= 0) {
+                const uint8_t* p = c.data + row * c.row_bytes;
                 if constexpr (kFp4) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(c.data + row * c.row_bytes + 8 * lane);
-                    q[u].x = w.x;
-                    q[u].z = w.y;
-                    s[u] = scale_value<FMT == EP_NVFP4>(c.scales[row * c.scale_bytes + (FMT == EP_NVFP4 ? lane : lane / 2)]);
-                } else {
-                    const uint8_t* p = c.data + row * c.row_bytes + e;
-                    if (c.head_dim % 16 == 0) {
-                        q[u] = *reinterpret_cast<const uint4*>(p);
-                    } else {
-                        const uint2 w0 = *reinterpret_cast<const uint2*>(p);
-                        q[u].x = w0.x, q[u].y = w0.y;
-                        if (second[u]) {
-                            const uint2 w1 = *reinterpret_cast<const uint2*>(p + 8);
-                            q[u].z = w1.x, q[u].w = w1.y;
-                        }
+                    constexpr int kPer = FMT == EP_NVFP4 ? 2 : 4;  // chunks of a block
+                    const uint8_t* sc = c.scales + row * c.scale_bytes;
+                    q[u][0].x = reinterpret_cast<const uint32_t*>(p)[lane];
+                    s[u][0] = scale_value<FMT == EP_NVFP4>(sc[lane / kPer]);
+                    if (second[u]) {
+                        q[u][1].x = reinterpret_cast<const uint32_t*>(p)[lane + LANES];
+                        s[u][1] = scale_value<FMT == EP_NVFP4>(sc[(lane + LANES) / kPer]);
                     }
-                    s[u] = reinterpret_cast<const float*>(c.scales)[row];
+                } else {
+                    q[u][0] = reinterpret_cast<const uint2*>(p)[lane];
+                    if (second[u]) q[u][1] = reinterpret_cast<const uint2*>(p)[lane + LANES];
+                    s[u][0] = reinterpret_cast<const float*>(c.scales)[row];
                 }
             }
         }
@@ -431,11 +426,11 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
         for (int u = 0; u < kBatch; ++u) {
             if (!dst[u]) continue;
             float v[8];
-            values8<FMT>(q[u].x, q[u].y, s[u], v);
+            values8<FMT>(q[u][0].x, q[u][0].y, s[u][0], v);
             store8<DT>(dst[u], 8, 16, v);
             if (second[u]) {
-                values8<FMT>(q[u].z, q[u].w, s[u], v);
-                store8<DT>(dst[u] + 8, 8, 16, v);
+                values8<FMT>(q[u][1].x, q[u][1].y, s[u][kFp4 ? 1 : 0], v);
+                store8<DT>(dst[u] + 8 * LANES, 8, 16, v);
             }
         }
     }
