@@ -6,6 +6,7 @@
 #include "blob.h"
 #include "microscale.cuh"
 #include "ops.h"
+#include "tcgen05.cuh"
 
 namespace ep {
 namespace {
@@ -20,8 +21,11 @@ using namespace ms;
 constexpr int kThreads = 256;
 constexpr int kMaxHeadDim = 1024;
 constexpr int kMaxFastDim = 256;
-constexpr int kLaunchTokens = 4096;  // tokens of one write launch
-constexpr int kMaxWriteTokens = 8;   // most tokens of one block of a write
+constexpr int kLaunchTokens = 16384; // tokens of one write launch
+constexpr int kMaxWriteTokens = 16;  // most tokens of one block of a write
+constexpr int kMaxCluster = 8;       // blocks of a write that look for repeated slots together
+constexpr int kAloneTokens = 1024;    // up to so many tokens a block looks for repeated slots alone
+constexpr int kTable = 512;          // hash table of their slots
 constexpr int kMaxReadTokens = 64;   // most tokens of one block of a read
 constexpr int kSharedSeqs = 1024;    // sequence starts that a read searches in shared memory
 
@@ -44,6 +48,7 @@ struct WriteArgs {
     int n, heads;         // caches, and heads of each
     float heads_inv;
     int per_block;        // tokens of one block
+    int cluster;          // blocks of one cluster
 };
 
 struct ReadArgs {
@@ -150,32 +155,73 @@ __device__ __forceinline__ uint2 payload8(const Raw8<DT>& v, float s, float inv)
 
 // Where a block's tokens go: a token's slot, or -1 for one that is skipped.  A token whose slot a later
 // token of the launch names again is dropped, so that payload and scale of a slot always come from one
-// token (launches of one call follow each other, the later wins).  All threads; ends with a barrier.
-__device__ __forceinline__ void find_slots(const WriteArgs& a, int64_t t0, int n, int64_t* slot, int* dropped) {
-    if (int(threadIdx.x) < n) {
-        const int64_t s = a.slots[t0 + threadIdx.x];
-        slot[threadIdx.x] = s >= 0 && s < a.n_slots ? s : -1;
-        dropped[threadIdx.x] = 0;
+// token (launches of one call follow each other, the later wins).  The blocks of a cluster do this for
+// all of its tokens: each puts their slots into a hash table and looks up its share of the tokens behind.
+// (16384 tokens in blocks of 16, each comparing what is behind with its own 16: 9 of 33 us.)
+struct SlotMemory {
+    int64_t slot[kMaxCluster * kMaxWriteTokens];
+    int dropped[kMaxCluster * kMaxWriteTokens];
+    int table[kTable];
+    int64_t mine[kMaxWriteTokens];
+};
+__device__ __forceinline__ uint32_t slot_hash(int64_t s) {
+    return ((uint32_t(s) ^ uint32_t(uint64_t(s) >> 32)) * 2654435761u) >> 23;
+}
+// Four of the launch's slots that a thread looks up, `step` apart.
+struct Later {
+    int64_t s[4];
+    __device__ __forceinline__ void load(const WriteArgs& a, int64_t j0, int64_t step) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[u] = j0 + u * step < a.tokens ? a.slots[j0 + u * step] : -1;
+    }
+};
+// All threads of the cluster: `own` is the slot of the group's token threadIdx.x, `later` the first four
+// slots to look up, both loaded before; leave_slots comes at the block's end.
+__device__ __forceinline__ void find_slots(const WriteArgs& a, int64_t first, int n, uint32_t rank, uint32_t ranks, int64_t own,
+                                           Later later, SlotMemory& m) {
+    static_assert(kTable == 1 << 9, "slot_hash gives 9 bits");
+    for (int i = threadIdx.x; i < kTable; i += kThreads) m.table[i] = -1;
+    if (own >= a.n_slots) own = -1;
+    if (threadIdx.x < kMaxCluster * kMaxWriteTokens) {
+        m.slot[threadIdx.x] = own;
+        m.dropped[threadIdx.x] = 0;
     }
     __syncthreads();
-    int64_t lo = a.n_slots, hi = -1;
-    for (int i = 0; i < n; ++i)
-        if (slot[i] >= 0) lo = min(lo, slot[i]), hi = max(hi, slot[i]);
-    const uint64_t span = uint64_t(hi - lo);
-    if (hi >= 0)
-        for (int64_t j0 = t0 + 1 + threadIdx.x; j0 < a.tokens; j0 += 4 * kThreads) {
-            int64_t s[4];
+    if (own >= 0)
+        for (uint32_t h = slot_hash(own); atomicCAS(&m.table[h], -1, int(threadIdx.x)) != -1;) h = (h + 1) % kTable;
+    __syncthreads();
+    const int64_t step = int64_t(ranks) * kThreads;
+    for (int64_t j0 = first + 1 + rank * kThreads + threadIdx.x; j0 < a.tokens; j0 += 4 * step) {
+        const Later now = later;
+        later.load(a, j0 + 4 * step, step);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) s[u] = j0 + u * kThreads < a.tokens ? a.slots[j0 + u * kThreads] : -1;
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (uint64_t(s[u] - lo) <= span)
-                    for (int i = 0; i < n; ++i)
-                        if (slot[i] == s[u] && t0 + i < j0 + u * kThreads) dropped[i] = 1;
+        for (int u = 0; u < 4; ++u) {
+            if (now.s[u] < 0) continue;
+            int i;
+            for (uint32_t h = slot_hash(now.s[u]); (i = m.table[h]) != -1; h = (h + 1) % kTable)
+                if (m.slot[i] == now.s[u] && first + i < j0 + u * step) m.dropped[i] = 1;
         }
+    }
+    const int at = int(rank) * a.per_block + int(threadIdx.x);
+    if (ranks == 1) {
+        __syncthreads();
+        if (int(threadIdx.x) < n) m.mine[threadIdx.x] = m.dropped[at] ? -1 : m.slot[at];
+    } else {
+        __syncwarp();
+        tc::cluster_sync();
+        if (int(threadIdx.x) < n) {
+            uint32_t dropped = 0;
+            for (uint32_t r = 0; r < ranks; ++r) dropped |= tc::peer_load_u32(tc::smem_addr(&m.dropped[at]), r);
+            m.mine[threadIdx.x] = dropped ? -1 : m.slot[at];
+        }
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
     __syncthreads();
-    if (int(threadIdx.x) < n && dropped[threadIdx.x]) slot[threadIdx.x] = -1;
-    __syncthreads();
+}
+__device__ __forceinline__ void leave_slots(uint32_t ranks) {
+    __syncwarp();
+    if (ranks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no one reads this block's memory any more
 }
 
 // A block takes a few tokens, all heads of all caches; rows go in batches of LANES lanes a row, whose loads
@@ -185,11 +231,11 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
     using T = typename Elem<DT>::T;
     constexpr int kBatch = DT == EP_F32 ? 2 : 4, kStep = kThreads / LANES;
     constexpr bool kFp4 = FMT == EP_MXFP4 || FMT == EP_NVFP4;
-    __shared__ int64_t slot[kMaxWriteTokens];
-    __shared__ int dropped[kMaxWriteTokens];
+    __shared__ SlotMemory m;
     wait_for_stream();
-    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
-    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
+    const uint32_t rank = tc::cluster_rank(), ranks = tc::cluster_ranks();
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block, first = t0 - int64_t(rank) * a.per_block;
+    const int n = int(max(int64_t(0), min(int64_t(a.per_block), a.tokens - t0)));
     const int rows = n * a.heads, all = a.n * rows;
     const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     // 4-bit: sixteen neighbours, of one block; 8-bit: twice eight, so that lanes touch neighbouring bytes
@@ -210,9 +256,13 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
         }
     };
     load(0);
-    find_slots(a, t0, n, slot, dropped);
+    const int group = int(min(int64_t(ranks) * a.per_block, a.tokens - first));
+    const int64_t own = int(threadIdx.x) < group ? a.slots[first + threadIdx.x] : -1;
+    Later later;
+    later.load(a, first + 1 + rank * kThreads + threadIdx.x, int64_t(ranks) * kThreads);
+    find_slots(a, first, n, rank, ranks, own, later, m);
     // every lane of a warp stays in the loop: rows past the end are zeros and not written
-    for (int base = 0;;) {
+    for (int base = 0; base < all;) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             if (base + u * kStep >= all) break;
@@ -222,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
             r -= ci ? rows : 0;
             const int i = in ? quotient(r, a.heads_inv) : 0, h = r - i * a.heads;
             const CacheView& c = a.c[ci];
-            const int64_t to = in ? slot[i] : -1, row = to * a.heads + h;
+            const int64_t to = in ? m.mine[i] : -1, row = to * a.heads + h;
             const bool live = to >= 0 && e < c.head_dim;
             uint32_t bits = max(abs_max8<DT>(v[u][0]), abs_max8<DT>(v[u][1]));
             if constexpr (kFp4) {
@@ -247,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
             }
         }
         base += kBatch * kStep;
-        if (base >= all) break;
-        load(base);
+        if (base < all) load(base);
     }
+    leave_slots(ranks);
 }
 
 // The same for any head: a warp a row, 4 chunks of 8 elements a lane, at any alignment.
@@ -257,17 +307,21 @@ template <int DT, int FMT>
 __global__ void __launch_bounds__(kThreads) cache_write_any_kernel(const __grid_constant__ WriteArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int NC = kMaxHeadDim / 256;
-    __shared__ int64_t slot[kMaxWriteTokens];
-    __shared__ int dropped[kMaxWriteTokens];
+    __shared__ SlotMemory m;
     wait_for_stream();
-    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
-    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
-    find_slots(a, t0, n, slot, dropped);
+    const uint32_t rank = tc::cluster_rank(), ranks = tc::cluster_ranks();
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block, first = t0 - int64_t(rank) * a.per_block;
+    const int n = int(max(int64_t(0), min(int64_t(a.per_block), a.tokens - t0)));
+    const int group = int(min(int64_t(ranks) * a.per_block, a.tokens - first));
+    const int64_t own = int(threadIdx.x) < group ? a.slots[first + threadIdx.x] : -1;
+    Later later;
+    later.load(a, first + 1 + rank * kThreads + threadIdx.x, int64_t(ranks) * kThreads);
+    find_slots(a, first, n, rank, ranks, own, later, m);
     const int rows = n * a.heads, lane = threadIdx.x % 32;
     for (int r = threadIdx.x / 32; r < a.n * rows; r += kThreads / 32) {
         const int ci = r >= rows, i = quotient(r - ci * rows, a.heads_inv), h = r - ci * rows - i * a.heads;
         const CacheView& c = a.c[ci];
-        const int64_t to = slot[i], row = to * a.heads + h;
+        const int64_t to = m.mine[i], row = to * a.heads + h;
         if (to < 0) continue;
         const T* src = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride;
         uint8_t* data = c.data + row * c.row_bytes;
@@ -308,6 +362,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_any_kernel(const __grid_
             }
         }
     }
+    leave_slots(ranks);
 }
 
 // ---- reading -----------------------------------------------------------------------------------
@@ -373,7 +428,7 @@ __device__ __forceinline__ void find_pages(const ReadArgs& a, int64_t t0, int n,
 // A block takes up to 64 tokens, all heads of all outputs: finds their slots, then reads rows of LANES
 // lanes in batches, whose loads are all on their way before the first is used.
 template <int DT, int FMT, int LANES>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) cache_read_kernel(const __grid_constant__ ReadArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int kBatch = 4, kStep = kThreads / LANES;
     constexpr bool kFp4 = FMT == EP_MXFP4 || FMT == EP_NVFP4;
@@ -492,7 +547,7 @@ cudaError_t launch_write(const WriteArgs& w, int lanes, dim3 grid, cudaStream_t 
                         : lanes == 8 ? cache_write_kernel<DT, FMT, 8>
                         : lanes == 16 ? cache_write_kernel<DT, FMT, 16>
                                       : cache_write_any_kernel<DT, FMT>;
-    return op::launch(kernel, grid, dim3(kThreads), 0, st, w);
+    return op::launch_clusters(kernel, grid, dim3(kThreads), 0, w.cluster, st, w);
 }
 template <int DT>
 cudaError_t write_as(int fmt, const WriteArgs& w, int lanes, dim3 grid, cudaStream_t st) {
@@ -600,8 +655,10 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
         for (int i = 0; i < n; ++i)
             part.c[i].heads = static_cast<uint8_t*>(w.c[i].heads) + t0 * w.c[i].token_stride * es;
         // few tokens are spread over the SMs
-        part.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxWriteTokens, part.tokens / (2 * sms))));
-        const dim3 grid(unsigned(op::div_up(part.tokens, part.per_block)));
+        part.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxWriteTokens, op::div_up(part.tokens, 4 * sms))));
+        // where most of a look through the launch's tokens is worth more than a cluster's barriers
+        part.cluster = part.tokens > kAloneTokens ? kMaxCluster : 1;
+        const dim3 grid(unsigned(op::div_up(part.tokens, int64_t(part.per_block) * part.cluster) * part.cluster));
         const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, lanes, grid, st)
                               : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, lanes, grid, st)
                                                         : write_as<EP_F32>(caches[0].format, part, lanes, grid, st);
@@ -636,7 +693,7 @@ extern "C" int ep_cache_read(const ep_cache* caches, const ep_heads* out, int n,
     r.heads_inv = 1.0f / float(r.heads);
     r.n = n;
     // few tokens are spread over the SMs
-    r.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxReadTokens, r.tokens / (4 * sms))));
+    r.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxReadTokens, op::div_up(r.tokens, 4 * sms))));
     const dim3 grid(unsigned(op::div_up(r.tokens, r.per_block)));
     const int lanes = lanes_of(r.c, n);
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -109,8 +109,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
     auto empty = [&](int s) { return bars + 8 * (G::kStages + s); };
     const uint32_t done = bars + 16 * G::kStages, slot = done + 8;
     const int warp = int(uniform(threadIdx.x / 32)), lane = threadIdx.x % 32;
-    uint32_t ranks, rank = cluster_rank();
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+    const uint32_t rank = cluster_rank(), ranks = cluster_ranks();
     const int tile = int(blockIdx.x / ranks);
     const int n0 = (tile % a.n_tiles) * 128, m0 = (tile / a.n_tiles) * NT;
     const int k0 = int(int64_t(a.steps) * rank / ranks), steps = int(int64_t(a.steps) * (rank + 1) / ranks) - k0;
@@ -609,20 +608,7 @@ int run_split(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& 
     const int64_t grid = tiles * split;
     if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: too many tiles");
     if (e == cudaSuccess) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(unsigned(grid));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = G::kSmem;
-        cfg.stream = st;
-        cudaLaunchAttribute at[2];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        at[1].id = cudaLaunchAttributeClusterDimension;
-        at[1].val.clusterDim.x = unsigned(split);
-        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 2;
-        e = cudaLaunchKernelEx(&cfg, fp4_split_kernel<NT, NV>, b_map, a_map, args);
+        e = op::launch_clusters(fp4_split_kernel<NT, NV>, dim3(unsigned(grid)), dim3(kThreads), G::kSmem, split, st, b_map, a_map, args);
     }
     if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_matmul: ") + cudaGetErrorString(e));
     return EP_OK;
