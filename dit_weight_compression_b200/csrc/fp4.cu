@@ -16,7 +16,7 @@ using namespace ms;
 constexpr int kTileRows = 128;   // a block handles 128 rows x 128 columns: whole 512-byte scale
 constexpr int kTileCols = 128;   // tiles (two for blocks of 16), written at once
 constexpr int kThreads = 256;
-constexpr int kPassRows = kThreads / (kTileCols / 8);  // 16 threads a row, 8 elements each
+constexpr int kPassRows = kThreads / (kTileCols / 8);  // dequantising: 16 threads a row, 8 elements each
 constexpr int kPasses = kTileRows / kPassRows;
 constexpr int kMaxPartials = EP_FP4_SCALE_FLOATS - 1;
 
@@ -93,57 +93,74 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(const QuantArgs a) {
     if (threadIdx.x == 0) a.tensor_scale[1 + blockIdx.x] = abs_value<DT>(m);
 }
 
-// One pass: a block reads its 128 x 128 elements (8 loads of 16 bytes a thread in flight), forms the
-// block scales among 2 or 4 neighbouring threads, writes 4 bytes of codes a thread and its scale tiles.
-template <int DT, bool NV>
-__global__ void __launch_bounds__(kThreads, 3) quantize_kernel(const QuantArgs a) {
+// One pass: a block reads its 128 x 128 elements, forms the block scales among neighbouring threads and
+// writes their codes and its scale tiles.  A thread has 16 neighbours of 16-bit elements (with 8, a scale
+// was formed 2 or 4 times over and issue took as long as the memory: 100 instructions for 8 elements and
+// 73 us for 8192 x 16384 bf16; now 58 and 60), but 8 of fp32 (16 are 64 bytes, too far from one thread
+// to the next: 40 us for 4096 x 11008, 37 with 8).  FAST: rows in whole sixteens, 16-byte aligned.
+template <int DT, bool NV, bool FAST>
+__global__ void __launch_bounds__(kThreads, 4) quantize_kernel(const __grid_constant__ QuantArgs a) {
     using T = typename Elem<DT>::T;
-    constexpr int kBatch = DT == EP_F32 ? kPasses / 2 : kPasses;
+    constexpr int kC = DT == EP_F32 ? 1 : 2;                        // chunks of 8 elements a thread
+    constexpr int kParts = kTileCols / (8 * kC);                    // threads a row
+    constexpr int kRows = kThreads / kParts, kSteps = kTileRows / kRows;
+    constexpr int kBatch = 4;                                       // steps in flight
+    constexpr int kOwners = (NV ? 16 : 32) / (8 * kC);              // threads of a scale block
     __shared__ uint32_t red[kThreads / 32];
     __shared__ __align__(16) uint8_t sc[NV ? 1024 : 512];
     wait_for_stream();
     const uint32_t block = a.backwards ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
     const uint32_t row_tile = block / uint32_t(a.col_tiles), col_tile = block - row_tile * uint32_t(a.col_tiles);
     const int64_t row0 = int64_t(row_tile) * kTileRows;
-    const int64_t col = int64_t(col_tile) * kTileCols + 8 * (threadIdx.x % 16);
-    const int sub = threadIdx.x / 16;
+    const int part = threadIdx.x % kParts, sub = threadIdx.x / kParts;
+    const int64_t col = int64_t(col_tile) * kTileCols + 8 * kC * part;
     const int rows = int(min(int64_t(kTileRows), a.rows - row0));
-    const int n = int(max(int64_t(0), min(int64_t(8), a.cols - col)));
+    const int n = int(max(int64_t(0), min(int64_t(8 * kC), a.cols - col)));
     const T* x = static_cast<const T*>(a.x) + (row0 + sub) * a.stride + col;
     uint8_t* data = a.data + (row0 + sub) * a.row_bytes + col / 2;
-    const int k = (threadIdx.x % 16) / (NV ? 2 : 4);  // the scale block's column in this tile
-    const bool scales = threadIdx.x % (NV ? 2 : 4) == 0, codes_in = col < 2 * a.row_bytes;
+    const bool codes_in = col < 2 * a.row_bytes;
+    const int k = part / kOwners;  // the scale block's column in this tile
 
     float g = 1.0f, g_inv = 1.0f;
-    Raw8<DT> v[kBatch];
+    Raw8<DT> v[kBatch][kC];
 #pragma unroll
-    for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+    for (int p0 = 0; p0 < kSteps; p0 += kBatch) {
 #pragma unroll
-        for (int p = 0; p < kBatch; ++p)
-            v[p] = load_raw8<DT>(x + int64_t(p0 + p) * kPassRows * a.stride, sub + (p0 + p) * kPassRows < rows ? n : 0, a.width);
+        for (int p = 0; p < kBatch; ++p) {
+            const T* src = x + int64_t(p0 + p) * kRows * a.stride;
+            const bool in = sub + (p0 + p) * kRows < rows;
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+                v[p][c] = FAST ? load_raw8<DT>(src + 8 * c, in && n ? 8 : 0, 16)
+                               : load_raw8<DT>(src + 8 * c, in ? min(n - 8 * c, 8) : 0, a.width);
+        }
         if (NV && p0 == 0) {
             if (a.fixed > 0.0f) {
                 g = a.fixed;
-            } else {
+            } else if (a.partials > 0) {
                 uint32_t m = 0;
-                if (a.partials > 0) {
-                    for (int i = threadIdx.x; i < a.partials; i += kThreads) m = max(m, __float_as_uint(a.tensor_scale[1 + i]));
-                    g = tensor_scale_of(__uint_as_float(block_max(m, red)));
-                } else {
-                    m = max_of_chunks<DT>(a, threadIdx.x, kThreads);
-                    g = tensor_scale_of(abs_value<DT>(block_max(m, red)));
-                }
+                for (int i = threadIdx.x; i < a.partials; i += kThreads) m = max(m, __float_as_uint(a.tensor_scale[1 + i]));
+                g = tensor_scale_of(__uint_as_float(block_max(m, red)));
+            } else {
+                g = tensor_scale_of(abs_value<DT>(block_max(max_of_chunks<DT>(a, threadIdx.x, kThreads), red)));
             }
             g_inv = pow2f(-log2_floor(g));
         }
 #pragma unroll
         for (int p = 0; p < kBatch; ++p) {
-            const int r = sub + (p0 + p) * kPassRows;
-            const Block b = block_scale<DT, NV>(lanes_max<NV ? 2 : 4>(abs_max8<DT>(v[p])), g, g_inv);
-            const uint32_t codes = quantize8<DT, NV>(v[p], b);
-            const bool in = r < rows;
-            if (in && codes_in) *reinterpret_cast<uint32_t*>(data + int64_t(p0 + p) * kPassRows * a.row_bytes) = codes;
-            if (scales) sc[(k / 4) * 512 + 16 * (r % 32) + 4 * (r / 32) + k % 4] = in && n > 0 ? b.byte : 0;
+            const bool in = sub + (p0 + p) * kRows < rows;
+            uint32_t m = abs_max8<DT>(v[p][0]);
+            if constexpr (kC == 2) m = max(m, abs_max8<DT>(v[p][1]));
+            const Block b = block_scale<DT, NV>(lanes_max<kOwners>(m), g, g_inv);
+            if (in && codes_in) {
+                uint8_t* to = data + int64_t(p0 + p) * kRows * a.row_bytes;
+                if constexpr (kC == 2)
+                    *reinterpret_cast<uint2*>(to) = make_uint2(quantize8<DT, NV>(v[p][0], b), quantize8<DT, NV>(v[p][1], b));
+                else
+                    *reinterpret_cast<uint32_t*>(to) = quantize8<DT, NV>(v[p][0], b);
+            }
+            const int r = sub + (p0 + p) * kRows;
+            if (part % kOwners == 0) sc[(k / 4) * 512 + k % 4 + 16 * (r % 32) + 4 * (r / 32)] = in && n ? b.byte : 0;
         }
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.tensor_scale[0] = g;
@@ -216,8 +233,10 @@ cudaError_t launch_quantize(const QuantArgs& q, bool nv, int64_t grid, int amax_
         cudaError_t e = op::launch(amax_kernel<DT>, dim3(unsigned(amax_grid)), dim3(kThreads), 0, st, q);
         if (e != cudaSuccess) return e;
     }
-    return op::launch(nv ? quantize_kernel<DT, true> : quantize_kernel<DT, false>, dim3(unsigned(grid)), dim3(kThreads), 0,
-                      st, q);
+    const bool fast = q.width == 16 && q.cols % 16 == 0;
+    const auto kernel = nv ? (fast ? quantize_kernel<DT, true, true> : quantize_kernel<DT, true, false>)
+                           : (fast ? quantize_kernel<DT, false, true> : quantize_kernel<DT, false, false>);
+    return op::launch(kernel, dim3(unsigned(grid)), dim3(kThreads), 0, st, q);
 }
 template <int DT>
 cudaError_t launch_dequantize(const DequantArgs& q, bool nv, int64_t grid, cudaStream_t st) {

@@ -19,7 +19,7 @@ import functools
 import torch
 
 from . import (FP8_E4M3, INT8, MXFP4, NVFP4, _TORCH_TO_EP, _check, _stream_handle, CompressedTensor, EpCache,
-               EpFP4Tensor, EpHeads, lib, tensor_view)
+               EpFP4Tensor, EpHeads, EpTensor, lib, tensor_view)
 
 FORMATS = {"mxfp4": MXFP4, "nvfp4": NVFP4}
 CACHE_FORMATS = {"fp8": FP8_E4M3, "int8": INT8, **FORMATS}
@@ -58,6 +58,16 @@ def _on(device: torch.device, stream):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _view(t: torch.Tensor) -> EpTensor:
+    """tensor_view without its repeated look-ups: these calls are a few microseconds long."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype not in _TORCH_TO_EP or (stride[1] != 1 and shape[1] > 1):
+        return tensor_view(t)  # raises
+    rows, cols = shape
+    return EpTensor(t.data_ptr(), t.get_device(), _TORCH_TO_EP[t.dtype], rows, cols,
+                    stride[0] if rows > 1 else cols)  # rows that overlap are refused by the library
 
 
 def _cuda(t: torch.Tensor, what: str, device: torch.device | None = None) -> torch.Tensor:
@@ -161,7 +171,7 @@ def fp4_quantize(x: torch.Tensor, format: str = "nvfp4", *, tensor_scale: float 
     """Quantise a 2-D CUDA tensor (bf16, fp16 or fp32; columns contiguous) with ep_fp4_quantize.
     `tensor_scale` (nvfp4 only): a power of two, else it is taken from the data in a pass of its own."""
     _cuda(x, "x")
-    view = tensor_view(x)
+    view = _view(x)
     ctx, st = _on(x.device, stream)
     with ctx:
         out = _made(x.shape, format, x.device, out, "fp4_quantize")
@@ -180,7 +190,7 @@ def fp4_dequantize(x: FP4Tensor, *, dtype: torch.dtype = torch.bfloat16, out: to
     ctx, st = _on(x.device, stream)
     with ctx:
         out = _dense(x.shape, dtype, x.device, out)
-        view = tensor_view(out)
+        view = _view(out)
         _check(lib().ep_fp4_dequantize(x._ref, ctypes.byref(view), st), "ep_fp4_dequantize")
     return out
 
@@ -198,7 +208,7 @@ def decompress_fp4(compressed: CompressedTensor, format: str = "nvfp4", *, tenso
     with ctx:
         out = _made(compressed.shape, format, dev, out, "decompress_fp4")
         work = _dense(compressed.shape, dtype, dev)
-        view = tensor_view(work)
+        view = _view(work)
         _check(lib().ep_decompress_fp4(compressed.handle, out._ref, 0.0 if tensor_scale is None else float(tensor_scale),
                                        ctypes.byref(view), st), "ep_decompress_fp4")
     return out
@@ -217,7 +227,7 @@ def fp4_matmul(a: FP4Tensor, b: FP4Tensor, *, bias: torch.Tensor | None = None, 
             if bias.dtype != out.dtype or tuple(bias.shape) != (b.shape[0],) or not bias.is_contiguous():
                 raise ValueError("fp4_matmul: bias must be a contiguous vector of the output's type, one element a row of b")
             p = bias.data_ptr()
-        view = tensor_view(out)
+        view = _view(out)
         _check(lib().ep_fp4_matmul(a._ref, b._ref, p, ctypes.byref(view), st), "ep_fp4_matmul")
     return out
 
@@ -273,14 +283,18 @@ class KVCache:
         return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scales, self.v_scales))
 
 
+_TwoHeads = EpHeads * 2
+
+
 def _heads(t: torch.Tensor, what: str) -> EpHeads:
-    if t.dim() != 3:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
         raise ValueError(f"{what} must be tokens x heads x head_dim")
     if t.dtype not in _TORCH_TO_EP:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if stride[2] != 1 and shape[2] > 1:
         raise ValueError(f"{what}: the elements of a head must be contiguous")
-    return EpHeads(t.data_ptr(), t.device.index, _TORCH_TO_EP[t.dtype], t.shape[0], t.shape[1], t.shape[2], t.stride(0), t.stride(1))
+    return EpHeads(t.data_ptr(), t.get_device(), _TORCH_TO_EP[t.dtype], *shape, stride[0], stride[1])
 
 
 def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *, stream=None) -> None:
@@ -291,7 +305,7 @@ def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
         _cuda(t, what, cache.device)
     if slots.dtype != torch.int64 or slots.dim() != 1 or slots.shape[0] != k.shape[0] or not slots.is_contiguous():
         raise ValueError("cache_write: slots must be a contiguous int64 vector with one entry a token")
-    views = (EpHeads * 2)(_heads(k, "k"), _heads(v, "v"))
+    views = _TwoHeads(_heads(k, "k"), _heads(v, "v"))
     ctx, st = _on(cache.device, stream)
     with ctx:
         _check(lib().ep_cache_write(cache._views, views, 2, slots.data_ptr(), st), "ep_cache_write")
@@ -321,7 +335,7 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, cu_seqlens: torch.Tenso
             out = (_dense(shape, dtype, cache.device), _dense(shape, dtype, cache.device))
         for t in out:
             _cuda(t, "out", cache.device)
-        views = (EpHeads * 2)(_heads(out[0], "out[0]"), _heads(out[1], "out[1]"))
+        views = _TwoHeads(_heads(out[0], "out[0]"), _heads(out[1], "out[1]"))
         _check(lib().ep_cache_read(cache._views, views, 2, page_table.data_ptr(),
                                    max(page_table.stride(0), page_table.shape[1]) if n > 1 else page_table.shape[1],
                                    page_table.shape[1], n, cu_seqlens.data_ptr(), st), "ep_cache_read")

@@ -371,6 +371,8 @@ def test_python_argument_errors(ep):
     with pytest.raises(ValueError):
         ep.fp4_quantize(x.T, "nvfp4")
     with pytest.raises(ep.EPError):
+        ep.fp4_quantize(x[:1].expand(4, 64), "nvfp4")     # rows that overlap
+    with pytest.raises(ep.EPError):
         ep.fp4_quantize(x, "mxfp4", tensor_scale=1.0)
     with pytest.raises(ep.EPError):
         ep.fp4_quantize(x.to(torch.int8), "nvfp4")
