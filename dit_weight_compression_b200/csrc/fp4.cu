@@ -97,9 +97,9 @@ __global__ void __launch_bounds__(kThreads) amax_kernel(const QuantArgs a) {
 // writes their codes and its scale tiles.  A thread has 16 neighbours of 16-bit elements (with 8, a scale
 // was formed 2 or 4 times over and issue took as long as the memory: 100 instructions for 8 elements and
 // 73 us for 8192 x 16384 bf16; now 58 and 60), but 8 of fp32 (16 are 64 bytes, too far from one thread
-// to the next: 40 us for 4096 x 11008, 37 with 8).  FAST: rows in whole sixteens, 16-byte aligned.
+// to the next: 40 us for 4096 x 11008, 36 with 8).  FAST: rows in whole sixteens, 16-byte aligned.
 template <int DT, bool NV, bool FAST>
-__global__ void __launch_bounds__(kThreads, 4) quantize_kernel(const __grid_constant__ QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, NV && DT == EP_F32 ? 3 : 4) quantize_kernel(const __grid_constant__ QuantArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int kC = DT == EP_F32 ? 1 : 2;                        // chunks of 8 elements a thread
     constexpr int kParts = kTileCols / (8 * kC);                    // threads a row
