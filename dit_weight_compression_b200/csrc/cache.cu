@@ -6,7 +6,6 @@
 #include "blob.h"
 #include "microscale.cuh"
 #include "ops.h"
-#include "tcgen05.cuh"
 
 namespace ep {
 namespace {
@@ -21,10 +20,11 @@ using namespace ms;
 constexpr int kThreads = 256;
 constexpr int kMaxHeadDim = 1024;
 constexpr int kMaxFastDim = 256;
-constexpr int kLaunchTokens = 16384; // tokens of one write launch
+constexpr int kLaunchTokens = 65536; // tokens of one write launch
 constexpr int kMaxWriteTokens = 16;  // most tokens of one block of a write
-constexpr int kMaxCluster = 8;       // blocks of a write that look for repeated slots together
-constexpr int kAloneTokens = 1024;    // up to so many tokens a block looks for repeated slots alone
+constexpr int kAloneTokens = 1024;   // up to so many tokens a write looks for repeated slots itself
+constexpr int kMendThreads = 1024;
+constexpr int kMendTokens = 128;     // tokens of one block of mend_kernel
 constexpr int kTable = 512;          // hash table of their slots
 constexpr int kMaxReadTokens = 64;   // most tokens of one block of a read
 constexpr int kSharedSeqs = 1024;    // sequence starts that a read searches in shared memory
@@ -48,7 +48,7 @@ struct WriteArgs {
     int n, heads;         // caches, and heads of each
     float heads_inv;
     int per_block;        // tokens of one block
-    int cluster;          // blocks of one cluster
+    bool alone;           // drop repeated slots here: no mend_kernel follows
 };
 
 struct ReadArgs {
@@ -153,75 +153,34 @@ __device__ __forceinline__ uint2 payload8(const Raw8<DT>& v, float s, float inv)
     else return int8_payload<DT>(v, s, inv);
 }
 
-// Where a block's tokens go: a token's slot, or -1 for one that is skipped.  A token whose slot a later
-// token of the launch names again is dropped, so that payload and scale of a slot always come from one
-// token (launches of one call follow each other, the later wins).  The blocks of a cluster do this for
-// all of its tokens: each puts their slots into a hash table and looks up its share of the tokens behind.
-// (16384 tokens in blocks of 16, each comparing what is behind with its own 16: 9 of 33 us.)
-struct SlotMemory {
-    int64_t slot[kMaxCluster * kMaxWriteTokens];
-    int dropped[kMaxCluster * kMaxWriteTokens];
-    int table[kTable];
-    int64_t mine[kMaxWriteTokens];
-};
-__device__ __forceinline__ uint32_t slot_hash(int64_t s) {
-    return ((uint32_t(s) ^ uint32_t(uint64_t(s) >> 32)) * 2654435761u) >> 23;
-}
-// Four of the launch's slots that a thread looks up, `step` apart.
-struct Later {
-    int64_t s[4];
-    __device__ __forceinline__ void load(const WriteArgs& a, int64_t j0, int64_t step) {
+// When a launch names a slot more than once, payload and scale have to come from one token, the last.
+// (Launches of one call follow each other, so that between launches the later wins.)  A write of few
+// tokens drops the others itself: every block compares its slots with all that come after.  For many
+// tokens that wait before the first store costs more than it brings (9 of 33 us for 16384), so the write
+// does not look, and mend_kernel, which finds the slots while the write's last blocks run, writes those
+// tokens once more.
+
+// Where a block's tokens go: their slots, -1 for one that is skipped.  All threads; ends with a barrier.
+__device__ __forceinline__ void find_slots(const WriteArgs& a, int64_t t0, int n, int64_t* slot, int* dropped) {
+    if (int(threadIdx.x) < n) {
+        const int64_t s = a.slots[t0 + threadIdx.x];
+        slot[threadIdx.x] = s >= 0 && s < a.n_slots ? s : -1;
+        dropped[threadIdx.x] = 0;
+    }
+    __syncthreads();
+    if (!a.alone) return;
+    for (int64_t j0 = t0 + 1 + threadIdx.x; j0 < a.tokens; j0 += 4 * kThreads) {
+        int64_t s[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) s[u] = j0 + u * step < a.tokens ? a.slots[j0 + u * step] : -1;
-    }
-};
-// All threads of the cluster: `own` is the slot of the group's token threadIdx.x, `later` the first four
-// slots to look up, both loaded before; leave_slots comes at the block's end.
-__device__ __forceinline__ void find_slots(const WriteArgs& a, int64_t first, int n, uint32_t rank, uint32_t ranks, int64_t own,
-                                           Later later, SlotMemory& m) {
-    static_assert(kTable == 1 << 9, "slot_hash gives 9 bits");
-    for (int i = threadIdx.x; i < kTable; i += kThreads) m.table[i] = -1;
-    if (own >= a.n_slots) own = -1;
-    if (threadIdx.x < kMaxCluster * kMaxWriteTokens) {
-        m.slot[threadIdx.x] = own;
-        m.dropped[threadIdx.x] = 0;
-    }
-    __syncthreads();
-    if (own >= 0)
-        for (uint32_t h = slot_hash(own); atomicCAS(&m.table[h], -1, int(threadIdx.x)) != -1;) h = (h + 1) % kTable;
-    __syncthreads();
-    const int64_t step = int64_t(ranks) * kThreads;
-    for (int64_t j0 = first + 1 + rank * kThreads + threadIdx.x; j0 < a.tokens; j0 += 4 * step) {
-        const Later now = later;
-        later.load(a, j0 + 4 * step, step);
+        for (int u = 0; u < 4; ++u) s[u] = j0 + u * kThreads < a.tokens ? a.slots[j0 + u * kThreads] : -1;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            if (now.s[u] < 0) continue;
-            int i;
-            for (uint32_t h = slot_hash(now.s[u]); (i = m.table[h]) != -1; h = (h + 1) % kTable)
-                if (m.slot[i] == now.s[u] && first + i < j0 + u * step) m.dropped[i] = 1;
-        }
-    }
-    const int at = int(rank) * a.per_block + int(threadIdx.x);
-    if (ranks == 1) {
-        __syncthreads();
-        if (int(threadIdx.x) < n) m.mine[threadIdx.x] = m.dropped[at] ? -1 : m.slot[at];
-    } else {
-        __syncwarp();
-        tc::cluster_sync();
-        if (int(threadIdx.x) < n) {
-            uint32_t dropped = 0;
-            for (uint32_t r = 0; r < ranks; ++r) dropped |= tc::peer_load_u32(tc::smem_addr(&m.dropped[at]), r);
-            m.mine[threadIdx.x] = dropped ? -1 : m.slot[at];
-        }
-        __syncwarp();
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        for (int u = 0; u < 4; ++u)
+            for (int i = 0; i < n; ++i)
+                if (s[u] >= 0 && slot[i] == s[u] && t0 + i < j0 + u * kThreads) dropped[i] = 1;
     }
     __syncthreads();
-}
-__device__ __forceinline__ void leave_slots(uint32_t ranks) {
-    __syncwarp();
-    if (ranks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no one reads this block's memory any more
+    if (int(threadIdx.x) < n && dropped[threadIdx.x]) slot[threadIdx.x] = -1;
+    __syncthreads();
 }
 
 // A block takes a few tokens, all heads of all caches; rows go in batches of LANES lanes a row, whose loads
@@ -231,11 +190,11 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
     using T = typename Elem<DT>::T;
     constexpr int kBatch = DT == EP_F32 ? 2 : 4, kStep = kThreads / LANES;
     constexpr bool kFp4 = FMT == EP_MXFP4 || FMT == EP_NVFP4;
-    __shared__ SlotMemory m;
+    __shared__ int64_t slot[kMaxWriteTokens];
+    __shared__ int dropped[kMaxWriteTokens];
     wait_for_stream();
-    const uint32_t rank = tc::cluster_rank(), ranks = tc::cluster_ranks();
-    const int64_t t0 = int64_t(blockIdx.x) * a.per_block, first = t0 - int64_t(rank) * a.per_block;
-    const int n = int(max(int64_t(0), min(int64_t(a.per_block), a.tokens - t0)));
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
+    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
     const int rows = n * a.heads, all = a.n * rows;
     const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     // 4-bit: sixteen neighbours, of one block; 8-bit: twice eight, so that lanes touch neighbouring bytes
@@ -256,11 +215,7 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
         }
     };
     load(0);
-    const int group = int(min(int64_t(ranks) * a.per_block, a.tokens - first));
-    const int64_t own = int(threadIdx.x) < group ? a.slots[first + threadIdx.x] : -1;
-    Later later;
-    later.load(a, first + 1 + rank * kThreads + threadIdx.x, int64_t(ranks) * kThreads);
-    find_slots(a, first, n, rank, ranks, own, later, m);
+    find_slots(a, t0, n, slot, dropped);
     // every lane of a warp stays in the loop: rows past the end are zeros and not written
     for (int base = 0; base < all;) {
 #pragma unroll
@@ -272,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
             r -= ci ? rows : 0;
             const int i = in ? quotient(r, a.heads_inv) : 0, h = r - i * a.heads;
             const CacheView& c = a.c[ci];
-            const int64_t to = in ? m.mine[i] : -1, row = to * a.heads + h;
+            const int64_t to = in ? slot[i] : -1, row = to * a.heads + h;
             const bool live = to >= 0 && e < c.head_dim;
             uint32_t bits = max(abs_max8<DT>(v[u][0]), abs_max8<DT>(v[u][1]));
             if constexpr (kFp4) {
@@ -299,70 +254,123 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
         base += kBatch * kStep;
         if (base < all) load(base);
     }
-    leave_slots(ranks);
 }
 
-// The same for any head: a warp a row, 4 chunks of 8 elements a lane, at any alignment.
+// One row of any head by a warp, 4 chunks of 8 elements a lane, at any alignment.
+template <int DT, int FMT>
+__device__ __forceinline__ void write_any_row(const CacheView& c, const typename Elem<DT>::T* src, int64_t row) {
+    constexpr int NC = kMaxHeadDim / 256;
+    const int lane = threadIdx.x % 32;
+    uint8_t* data = c.data + row * c.row_bytes;
+    Raw8<DT> v[NC];
+#pragma unroll
+    for (int k = 0; k < NC; ++k) v[k] = load_raw8<DT>(src + 8 * (lane + 32 * k), min(8, c.head_dim - 8 * (lane + 32 * k)), c.width);
+    if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
+        uint32_t bits = 0;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) bits = max(bits, abs_max8<DT>(v[k]));
+        float s, inv;
+        row_scale<DT, FMT>(lanes_max<32>(bits), s, inv);
+        if (lane == 0) reinterpret_cast<float*>(c.scales)[row] = s;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            const int at = 8 * (lane + 32 * k);
+            if (at >= c.head_dim) break;
+            const uint2 w = payload8<DT, FMT>(v[k], s, inv);
+            if (c.head_dim % 8 == 0) {
+                *reinterpret_cast<uint2*>(data + at) = w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (at + j < c.head_dim) data[at + j] = uint8_t((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
+            }
+        }
+    } else {
+        constexpr bool NV = FMT == EP_NVFP4;
+#pragma unroll
+        for (int k = 0; k < NC; ++k) {
+            const int chunk = lane + 32 * k;
+            const Block b = block_scale<DT, NV>(lanes_max<NV ? 2 : 4>(abs_max8<DT>(v[k])), 1.0f, 1.0f);
+            const uint32_t codes = quantize8<DT, NV>(v[k], b);
+            if (4 * chunk >= int(c.row_bytes)) continue;
+            *reinterpret_cast<uint32_t*>(data + 4 * chunk) = codes;
+            if (chunk % (NV ? 2 : 4) == 0 && 8 * chunk < c.head_dim)
+                c.scales[row * c.scale_bytes + chunk / (NV ? 2 : 4)] = uint8_t(b.byte);
+        }
+    }
+}
+
+// cache_write_kernel for any head: a warp a row.
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kThreads) cache_write_any_kernel(const __grid_constant__ WriteArgs a) {
     using T = typename Elem<DT>::T;
-    constexpr int NC = kMaxHeadDim / 256;
-    __shared__ SlotMemory m;
+    __shared__ int64_t slot[kMaxWriteTokens];
+    __shared__ int dropped[kMaxWriteTokens];
     wait_for_stream();
-    const uint32_t rank = tc::cluster_rank(), ranks = tc::cluster_ranks();
-    const int64_t t0 = int64_t(blockIdx.x) * a.per_block, first = t0 - int64_t(rank) * a.per_block;
-    const int n = int(max(int64_t(0), min(int64_t(a.per_block), a.tokens - t0)));
-    const int group = int(min(int64_t(ranks) * a.per_block, a.tokens - first));
-    const int64_t own = int(threadIdx.x) < group ? a.slots[first + threadIdx.x] : -1;
-    Later later;
-    later.load(a, first + 1 + rank * kThreads + threadIdx.x, int64_t(ranks) * kThreads);
-    find_slots(a, first, n, rank, ranks, own, later, m);
-    const int rows = n * a.heads, lane = threadIdx.x % 32;
+    const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
+    const int n = int(min(int64_t(a.per_block), a.tokens - t0));
+    find_slots(a, t0, n, slot, dropped);
+    const int rows = n * a.heads;
     for (int r = threadIdx.x / 32; r < a.n * rows; r += kThreads / 32) {
         const int ci = r >= rows, i = quotient(r - ci * rows, a.heads_inv), h = r - ci * rows - i * a.heads;
         const CacheView& c = a.c[ci];
-        const int64_t to = m.mine[i], row = to * a.heads + h;
-        if (to < 0) continue;
-        const T* src = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride;
-        uint8_t* data = c.data + row * c.row_bytes;
-        Raw8<DT> v[NC];
+        if (slot[i] >= 0)
+            write_any_row<DT, FMT>(c, static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride,
+                                   slot[i] * a.heads + h);
+    }
+}
+
+// After a write that did not look: each block puts the slots of 128 tokens into a hash table, looks up all
+// slots of the launch, and writes those of its tokens again that come last of several to a slot.
+__device__ __forceinline__ uint32_t slot_hash(int64_t s) {
+    static_assert(kTable == 1 << 9, "9 bits");
+    return ((uint32_t(s) ^ uint32_t(uint64_t(s) >> 32)) * 2654435761u) >> 23;
+}
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kMendThreads) mend_kernel(const __grid_constant__ WriteArgs a) {
+    using T = typename Elem<DT>::T;
+    __shared__ int64_t slot[kMendTokens];
+    __shared__ int earlier[kMendTokens], later[kMendTokens], table[kTable], any;
+    const int64_t t0 = int64_t(blockIdx.x) * kMendTokens;
+    const int n = int(min(int64_t(kMendTokens), a.tokens - t0));
+    // The slots are read before the write is waited for: the write itself started only when everything
+    // before it was done, and does not change them.  (From L2: nothing older is taken.)
+    int64_t own = -1;
+    if (int(threadIdx.x) < n) {
+        own = __ldcg(a.slots + t0 + threadIdx.x);
+        if (own >= a.n_slots) own = -1;
+        slot[threadIdx.x] = own;
+        earlier[threadIdx.x] = later[threadIdx.x] = 0;
+    }
+    if (threadIdx.x < kTable) table[threadIdx.x] = -1;
+    if (threadIdx.x == 0) any = 0;
+    __syncthreads();
+    if (own >= 0)
+        for (uint32_t h = slot_hash(own); atomicCAS(&table[h], -1, int(threadIdx.x)) != -1;) h = (h + 1) % kTable;
+    __syncthreads();
+    for (int64_t j0 = threadIdx.x; j0 < a.tokens; j0 += 8 * kMendThreads) {
+        int64_t s[8];
 #pragma unroll
-        for (int k = 0; k < NC; ++k) v[k] = load_raw8<DT>(src + 8 * (lane + 32 * k), min(8, c.head_dim - 8 * (lane + 32 * k)), c.width);
-        if constexpr (FMT == EP_FP8_E4M3 || FMT == EP_INT8) {
-            uint32_t bits = 0;
+        for (int u = 0; u < 8; ++u) s[u] = j0 + u * kMendThreads < a.tokens ? __ldcg(a.slots + j0 + u * kMendThreads) : -1;
 #pragma unroll
-            for (int k = 0; k < NC; ++k) bits = max(bits, abs_max8<DT>(v[k]));
-            float s, inv;
-            row_scale<DT, FMT>(lanes_max<32>(bits), s, inv);
-            if (lane == 0) reinterpret_cast<float*>(c.scales)[row] = s;
-#pragma unroll
-            for (int k = 0; k < NC; ++k) {
-                const int at = 8 * (lane + 32 * k);
-                if (at >= c.head_dim) break;
-                const uint2 w = payload8<DT, FMT>(v[k], s, inv);
-                if (c.head_dim % 8 == 0) {
-                    *reinterpret_cast<uint2*>(data + at) = w;
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (at + j < c.head_dim) data[at + j] = uint8_t((j < 4 ? w.x : w.y) >> (8 * (j % 4)));
-                }
-            }
-        } else {
-            constexpr bool NV = FMT == EP_NVFP4;
-#pragma unroll
-            for (int k = 0; k < NC; ++k) {
-                const int chunk = lane + 32 * k;
-                const Block b = block_scale<DT, NV>(lanes_max<NV ? 2 : 4>(abs_max8<DT>(v[k])), 1.0f, 1.0f);
-                const uint32_t codes = quantize8<DT, NV>(v[k], b);
-                if (4 * chunk >= int(c.row_bytes)) continue;
-                *reinterpret_cast<uint32_t*>(data + 4 * chunk) = codes;
-                if (chunk % (NV ? 2 : 4) == 0 && 8 * chunk < c.head_dim)
-                    c.scales[row * c.scale_bytes + chunk / (NV ? 2 : 4)] = uint8_t(b.byte);
-            }
+        for (int u = 0; u < 8; ++u) {
+            if (s[u] < 0) continue;
+            const int64_t j = j0 + u * kMendThreads - t0;
+            int i;
+            for (uint32_t h = slot_hash(s[u]); (i = table[h]) != -1; h = (h + 1) % kTable)
+                if (slot[i] == s[u] && j != i) (j < i ? earlier : later)[i] = any = 1;
         }
     }
-    leave_slots(ranks);
+    __syncthreads();
+    wait_for_stream();
+    if (!any) return;
+    for (int r = threadIdx.x / 32; r < a.n * n * a.heads; r += kMendThreads / 32) {
+        const int i = r / (a.n * a.heads), rest = r - i * a.n * a.heads, ci = rest / a.heads, h = rest - ci * a.heads;
+        const CacheView& c = a.c[ci];
+        if (earlier[i] && !later[i])
+            write_any_row<DT, FMT>(c, static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride,
+                                   slot[i] * a.heads + h);
+    }
 }
 
 // ---- reading -----------------------------------------------------------------------------------
@@ -547,7 +555,9 @@ cudaError_t launch_write(const WriteArgs& w, int lanes, dim3 grid, cudaStream_t 
                         : lanes == 8 ? cache_write_kernel<DT, FMT, 8>
                         : lanes == 16 ? cache_write_kernel<DT, FMT, 16>
                                       : cache_write_any_kernel<DT, FMT>;
-    return op::launch_clusters(kernel, grid, dim3(kThreads), 0, w.cluster, st, w);
+    const cudaError_t e = op::launch(kernel, grid, dim3(kThreads), 0, st, w);
+    if (e != cudaSuccess || w.alone) return e;
+    return op::launch(mend_kernel<DT, FMT>, dim3(unsigned(op::div_up(w.tokens, kMendTokens))), dim3(kMendThreads), 0, st, w);
 }
 template <int DT>
 cudaError_t write_as(int fmt, const WriteArgs& w, int lanes, dim3 grid, cudaStream_t st) {
@@ -656,9 +666,8 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
             part.c[i].heads = static_cast<uint8_t*>(w.c[i].heads) + t0 * w.c[i].token_stride * es;
         // few tokens are spread over the SMs
         part.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxWriteTokens, op::div_up(part.tokens, 4 * sms))));
-        // where most of a look through the launch's tokens is worth more than a cluster's barriers
-        part.cluster = part.tokens > kAloneTokens ? kMaxCluster : 1;
-        const dim3 grid(unsigned(op::div_up(part.tokens, int64_t(part.per_block) * part.cluster) * part.cluster));
+        part.alone = part.tokens <= kAloneTokens;
+        const dim3 grid(unsigned(op::div_up(part.tokens, part.per_block)));
         const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, lanes, grid, st)
                               : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, lanes, grid, st)
                                                         : write_as<EP_F32>(caches[0].format, part, lanes, grid, st);

@@ -577,7 +577,9 @@ int run_pairs(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& 
     PairArgs p = {args};
     p.a_tiles = int(op::div_up(a->rows, 256));
     p.b_tiles = int(op::div_up(b->rows, 256));
-    p.group = 8;
+    // as many tiles of a as keep within about a quarter of L2; b's are then read from memory once for every
+    // `group` of them (8192 x 28672 x 8192: 745 us with 4, 710 with 8, 691 with 16, 694 with 32)
+    p.group = int(std::max<int64_t>(4, std::min<int64_t>(16, (int64_t(32) << 20) / (256 * op::fp4_row_bytes(a->cols)))));
     if (int64_t(p.a_tiles) * p.b_tiles > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: too many tiles");
     int pairs = 0;
     cudaError_t e = pairs_of<NV>(dev, pairs);

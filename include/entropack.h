@@ -320,7 +320,8 @@ typedef struct {
  *   slots   one int64 slot a token, device memory.  A token whose slot is negative or past the last
  *           page is skipped (padding).  When a slot is named more than once, the last token that
  *           names it is the one that is kept, in every cache.
- *   stream  cudaStream_t as void*; asynchronous; one kernel per 16384 tokens, no work space.
+ *   stream  cudaStream_t as void*; asynchronous; one kernel for up to 1024 tokens, two for each
+ *           65536 otherwise, no work space.
  * Other slots are left as they are.  Returns EP_ERR_ARG, EP_ERR_DTYPE, EP_ERR_SHAPE, EP_ERR_CUDA.
  */
 int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n, const int64_t* slots, void* stream);

@@ -149,7 +149,7 @@ def test_int8_borders(ep):
     check_slots(cache, slots.tolist(), x, -x)
 
 
-@pytest.mark.parametrize("n", [3, 600, 9000, 40000])
+@pytest.mark.parametrize("n", [3, 600, 1024, 1025, 9000, 70000])
 def test_skipped_and_repeated_slots(ep, n):
     """Padding (-1), slots past the last page, and slots named more than once: the last token wins, within a
     launch and across the launches of a long call."""
