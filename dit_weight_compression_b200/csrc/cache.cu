@@ -24,8 +24,9 @@ constexpr int kLaunchTokens = 65536; // tokens of one write launch
 constexpr int kMaxWriteTokens = 16;  // most tokens of one block of a write
 constexpr int kAloneTokens = 1024;   // up to so many tokens a write looks for repeated slots itself
 constexpr int kMendThreads = 1024;
-constexpr int kMendTokens = 128;     // tokens of one block of mend_kernel
-constexpr int kTable = 512;          // hash table of their slots
+constexpr int kMendTokens = 512;     // tokens of one block of mend_kernel
+constexpr int kTableBits = 11;       // hash table of their slots
+constexpr int kTable = 1 << kTableBits;
 constexpr int kMaxReadTokens = 64;   // most tokens of one block of a read
 constexpr int kSharedSeqs = 1024;    // sequence starts that a read searches in shared memory
 
@@ -320,15 +321,15 @@ __global__ void __launch_bounds__(kThreads) cache_write_any_kernel(const __grid_
     }
 }
 
-// After a write that did not look: each block puts the slots of 128 tokens into a hash table, looks up all
+// After a write that did not look: each block puts the slots of 512 tokens into a hash table, looks up all
 // slots of the launch, and writes those of its tokens again that come last of several to a slot.
 __device__ __forceinline__ uint32_t slot_hash(int64_t s) {
-    static_assert(kTable == 1 << 9, "9 bits");
-    return ((uint32_t(s) ^ uint32_t(uint64_t(s) >> 32)) * 2654435761u) >> 23;
+    return ((uint32_t(s) ^ uint32_t(uint64_t(s) >> 32)) * 2654435761u) >> (32 - kTableBits);
 }
 template <int DT, int FMT>
 __global__ void __launch_bounds__(kMendThreads) mend_kernel(const __grid_constant__ WriteArgs a) {
     using T = typename Elem<DT>::T;
+    static_assert(kMendThreads >= kMendTokens && 2 * kMendTokens <= kTable, "a thread for each token, and room in the table");
     __shared__ int64_t slot[kMendTokens];
     __shared__ int earlier[kMendTokens], later[kMendTokens], table[kTable], any;
     const int64_t t0 = int64_t(blockIdx.x) * kMendTokens;
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kMendThreads) mend_kernel(const __grid_constan
         slot[threadIdx.x] = own;
         earlier[threadIdx.x] = later[threadIdx.x] = 0;
     }
-    if (threadIdx.x < kTable) table[threadIdx.x] = -1;
+    for (int i = threadIdx.x; i < kTable; i += kMendThreads) table[i] = -1;
     if (threadIdx.x == 0) any = 0;
     __syncthreads();
     if (own >= 0)
@@ -664,8 +665,10 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
         part.tokens = std::min<int64_t>(kLaunchTokens, tokens - t0);
         for (int i = 0; i < n; ++i)
             part.c[i].heads = static_cast<uint8_t*>(w.c[i].heads) + t0 * w.c[i].token_stride * es;
-        // few tokens are spread over the SMs
-        part.per_block = int(std::max<int64_t>(1, std::min<int64_t>(kMaxWriteTokens, op::div_up(part.tokens, 4 * sms))));
+        // a block's rows are one batch of its threads (16384 tokens of 8 heads of 128, int8: 27 us with 8
+        // tokens a block, 30 with 16); few tokens are spread over the SMs
+        const int batch = 4 * kThreads / std::max(lanes, 4) / (w.heads * n);
+        part.per_block = int(std::max<int64_t>(1, std::min<int64_t>({kMaxWriteTokens, batch, op::div_up(part.tokens, 4 * sms)})));
         part.alone = part.tokens <= kAloneTokens;
         const dim3 grid(unsigned(op::div_up(part.tokens, part.per_block)));
         const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, lanes, grid, st)

@@ -48,13 +48,14 @@ class _Here:
 
 
 _HERE = _Here()
+_current_device = torch.cuda.current_device
 
 
 def _on(device: torch.device, stream):
     """(context in which `device` is current and temporaries belong to the call's stream, its handle)."""
     index = device.index
     if stream is None:
-        return (_HERE if index == torch.cuda.current_device() else torch.cuda.device(device)), _raw_stream(index)
+        return (_HERE if index == _current_device() else torch.cuda.device(device)), _raw_stream(index)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream), stream.cuda_stream
@@ -152,7 +153,7 @@ class FP4Tensor:
                     t.data[:, cols // 2] &= 15
             i, j = t._scale_tiles
             s = torch.zeros(i * 128, j * 4, dtype=torch.uint8, device=dev)
-            s[:rows, :blocks] = scale_rows
+            s[:rows, :blocks] = scale_rows if format == "mxfp4" else scale_rows & 0x7F  # E4M3 scales have no sign
             t.scales.copy_(s.view(i, 4, 32, j, 4).permute(0, 3, 2, 1, 4).reshape(-1))
             t.tensor_scale.copy_(tensor_scale.reshape(1))
         return t
@@ -337,7 +338,7 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, cu_seqlens: torch.Tenso
             _cuda(t, "out", cache.device)
         views = _TwoHeads(_heads(out[0], "out[0]"), _heads(out[1], "out[1]"))
         _check(lib().ep_cache_read(cache._views, views, 2, page_table.data_ptr(),
-                                   max(page_table.stride(0), page_table.shape[1]) if n > 1 else page_table.shape[1],
+                                   page_table.stride(0) if n > 1 else page_table.shape[1],
                                    page_table.shape[1], n, cu_seqlens.data_ptr(), st), "ep_cache_read")
     return out
 

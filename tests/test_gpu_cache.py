@@ -309,5 +309,11 @@ def test_python_argument_errors(ep):
         ep.cache_read(cache, t, torch.zeros(3, dtype=torch.int32, device="cuda"), total=1)
     with pytest.raises(ValueError):
         ep.cache_read(cache, t, torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ep.EPError):  # rows of the table that overlap
+        ep.cache_read(cache, t.expand(3, 2), torch.zeros(4, dtype=torch.int32, device="cuda"), total=1)
     with pytest.raises(ValueError):
         ep.KVCache.from_tensors(cache.k, cache.v_scales, cache.v, cache.v_scales[:1], "fp8", 64)
+    with pytest.raises(ep.EPError):  # outputs of two types, and of two lengths
+        ep.cache_read(cache, t, torch.zeros(2, dtype=torch.int32, device="cuda"), out=(x, x.float()))
+    with pytest.raises(ep.EPError):
+        ep.cache_read(cache, t, torch.zeros(2, dtype=torch.int32, device="cuda"), out=(x, x[:2]))

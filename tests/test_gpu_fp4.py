@@ -6,11 +6,17 @@ result is exact whatever the order; with general scales a sum of K / block float
 block, is off by at most (K / block) * 2^-23 * sum |a b| (one truncation a step), plus 2^-24 relative for each of the
 three factors of the scaling and half a step of the output's type.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
 import microscale_ref as R
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 pytestmark = pytest.mark.gpu
 FMTS = ["mxfp4", "nvfp4"]
@@ -355,6 +361,22 @@ def test_streams_and_graphs(ep):
         s.synchronize()
         assert torch.equal(y, want[1]) and torch.equal(d, ep.fp4_dequantize(q))
     ep.op_status()
+
+
+def test_first_calls_in_a_capture(ep):
+    """A process whose first product of every kind is captured: the look-ups that a first call makes are
+    none that a capture forbids."""
+    code = (
+        "import torch, dit_weight_compression_b200 as ep\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "x = torch.randn(700, 512, device='cuda'); w = torch.randn(4096, 512, device='cuda')\n"
+        "with torch.cuda.graph(g):\n"
+        "    ys = [ep.fp4_matmul(ep.fp4_quantize(x[:m], f), ep.fp4_quantize(w, f)) for f in ('mxfp4', 'nvfp4') for m in (1, 20, 50, 100, 700)]\n"
+        "g.replay(); torch.cuda.synchronize(); ep.op_status()\n"
+        "for y, (f, m) in zip(ys, [(f, m) for f in ('mxfp4', 'nvfp4') for m in (1, 20, 50, 100, 700)]):\n"
+        "    assert torch.equal(y, ep.fp4_matmul(ep.fp4_quantize(x[:m], f), ep.fp4_quantize(w, f)))\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_python_argument_errors(ep):
