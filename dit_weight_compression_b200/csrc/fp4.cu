@@ -83,9 +83,10 @@ __device__ __forceinline__ uint32_t max_of_chunks(const QuantArgs& a, int64_t fi
     return m;
 }
 
-// First pass over x for a tensor scale: block i's maximum goes to tensor_scale[1 + i].
+// First pass over x for a tensor scale: block i's maximum goes to tensor_scale[1 + i].  Bound by memory
+// (5.6 TB/s of 8192 x 11008 bf16).
 template <int DT>
-__global__ void __launch_bounds__(kThreads) amax_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 4 : 6) amax_kernel(const QuantArgs a) {
     __shared__ uint32_t smem[kThreads / 32];
     wait_for_stream();
     const uint32_t m = block_max(
@@ -245,9 +246,9 @@ cudaError_t launch_dequantize(const DequantArgs& q, bool nv, int64_t grid, cudaS
 }
 
 // Tensors of at most this many bytes are searched for their largest value by every block itself
-// (from L2, one launch); larger ones in a pass of their own.  1 x 8192 bf16 with the search in each
-// of its 64 blocks: see the table of measurements beside ep_fp4_quantize below.
-constexpr int64_t kSearchBytes = 128 << 10;
+// (from L2, one launch); larger ones in a pass of their own.  (bf16: 16 KB 2.9 us with the search, 4.1
+// with a pass; 64 KB 5.4 and 4.0; fp32: 32 KB 4.4 and 5.5, 128 KB 8.5 and 5.3.)
+constexpr int64_t kSearchBytes = 32 << 10;
 
 int check_dense(const ep_tensor* t, const char* what, const char* who) {
     const std::string w = std::string(who) + ": " + what;
@@ -313,7 +314,10 @@ int quantize(const ep_tensor* x, const ep_fp4_tensor* out, double tensor_scale, 
         if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, std::string(who) + ": the matrix is too large");
         int amax_grid = 0;
         if (nv && tensor_scale == 0.0 && x->rows * x->cols * es > kSearchBytes) {
-            amax_grid = int(std::min<int64_t>({kMaxPartials, 4 * int64_t(sms), op::div_up(x->rows * x->cols, 8 * 4 * kThreads)}));
+            // one round of blocks: 6 an SM for 16-bit elements, 4 for fp32 (8192 x 11008 bf16 in all: 83 us
+            // with 4, 74 with 6; 4096 x 11008 fp32: 70 and 77)
+            const int64_t per_sm = x->dtype == EP_F32 ? 4 : 6;
+            amax_grid = int(std::min<int64_t>({kMaxPartials, per_sm * sms, op::div_up(x->rows * x->cols, 8 * 4 * kThreads)}));
             q.partials = amax_grid;
             q.backwards = true;  // what the first pass read last is still in L2
         }
