@@ -181,8 +181,15 @@ def fp4_quantize(x: torch.Tensor, format: str = "nvfp4", *, tensor_scale: float 
     return out
 
 
-def _dense(shape, dtype, device, out=None) -> torch.Tensor:
-    return torch.empty(shape, dtype=dtype, device=device) if out is None else out
+def _dense(shape, dtype, device, out=None):
+    """(`out`, or a new tensor, and its C view)."""
+    if out is not None:
+        return out, _view(out)
+    if dtype not in _TORCH_TO_EP:
+        raise TypeError(f"unsupported dtype {dtype}")
+    rows, cols = shape
+    out = torch.empty(rows, cols, dtype=dtype, device=device)
+    return out, EpTensor(out.data_ptr(), device.index, _TORCH_TO_EP[dtype], rows, cols, cols)
 
 
 def fp4_dequantize(x: FP4Tensor, *, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
@@ -190,8 +197,7 @@ def fp4_dequantize(x: FP4Tensor, *, dtype: torch.dtype = torch.bfloat16, out: to
     """The values of a 4-bit tensor as a bf16, fp16 or fp32 tensor (ep_fp4_dequantize)."""
     ctx, st = _on(x.device, stream)
     with ctx:
-        out = _dense(x.shape, dtype, x.device, out)
-        view = _view(out)
+        out, view = _dense(x.shape, dtype, x.device, out)
         _check(lib().ep_fp4_dequantize(x._ref, ctypes.byref(view), st), "ep_fp4_dequantize")
     return out
 
@@ -208,8 +214,7 @@ def decompress_fp4(compressed: CompressedTensor, format: str = "nvfp4", *, tenso
     ctx, st = _on(dev, stream)
     with ctx:
         out = _made(compressed.shape, format, dev, out, "decompress_fp4")
-        work = _dense(compressed.shape, dtype, dev)
-        view = _view(work)
+        work, view = _dense(compressed.shape, dtype, dev)
         _check(lib().ep_decompress_fp4(compressed.handle, out._ref, 0.0 if tensor_scale is None else float(tensor_scale),
                                        ctypes.byref(view), st), "ep_decompress_fp4")
     return out
@@ -221,14 +226,13 @@ def fp4_matmul(a: FP4Tensor, b: FP4Tensor, *, bias: torch.Tensor | None = None, 
     `bias` has one element a row of b, of the output's type."""
     ctx, st = _on(a.device, stream)
     with ctx:
-        out = _dense((a.shape[0], b.shape[0]), dtype, a.device, out)
+        out, view = _dense((a.shape[0], b.shape[0]), dtype, a.device, out)
         p = None
         if bias is not None:
             _cuda(bias, "bias", a.device)
             if bias.dtype != out.dtype or tuple(bias.shape) != (b.shape[0],) or not bias.is_contiguous():
                 raise ValueError("fp4_matmul: bias must be a contiguous vector of the output's type, one element a row of b")
             p = bias.data_ptr()
-        view = _view(out)
         _check(lib().ep_fp4_matmul(a._ref, b._ref, p, ctypes.byref(view), st), "ep_fp4_matmul")
     return out
 
@@ -332,8 +336,8 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, cu_seqlens: torch.Tenso
     ctx, st = _on(cache.device, stream)
     with ctx:
         if out is None:
-            shape = (int(total), cache.heads, cache.head_dim)
-            out = (_dense(shape, dtype, cache.device), _dense(shape, dtype, cache.device))
+            rows, h, d, dev = int(total), cache.heads, cache.head_dim, cache.device
+            out = (torch.empty(rows, h, d, dtype=dtype, device=dev), torch.empty(rows, h, d, dtype=dtype, device=dev))
         for t in out:
             _cuda(t, "out", cache.device)
         views = _TwoHeads(_heads(out[0], "out[0]"), _heads(out[1], "out[1]"))
