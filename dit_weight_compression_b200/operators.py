@@ -10,6 +10,8 @@ and every call is asynchronous on the current stream of that device (or on ``str
     cache = ep.KVCache(n_pages, page_size, heads, head_dim, "fp8")
     ep.cache_write(cache, k, v, slots)            # k, v: tokens x heads x head_dim
     k, v = ep.cache_read(cache, page_table, cu_seqlens, total=n)
+
+They serve inference: no gradients flow through them.
 """
 from __future__ import annotations
 
@@ -268,7 +270,7 @@ class KVCache:
         return c
 
     def _set(self, k, k_scales, v, v_scales, format, head_dim):
-        self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
+        self._pools = (k, k_scales, v, v_scales)  # kept for as long as the pointers in _views
         self.format, self.head_dim, self.device = format, int(head_dim), k.device
         row, dt, scales, sdt = self._row(self.head_dim, format)
         if k.dim() != 4:
@@ -283,9 +285,14 @@ class KVCache:
                                               self.page_size, self.heads, self.head_dim)
                                       for p, s in ((k, k_scales), (v, v_scales))])
 
+    k = property(lambda self: self._pools[0])
+    k_scales = property(lambda self: self._pools[1])
+    v = property(lambda self: self._pools[2])
+    v_scales = property(lambda self: self._pools[3])
+
     @property
     def nbytes(self) -> int:
-        return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scales, self.v_scales))
+        return sum(t.numel() * t.element_size() for t in self._pools)
 
 
 _TwoHeads = EpHeads * 2
