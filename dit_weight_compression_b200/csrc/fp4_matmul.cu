@@ -131,6 +131,17 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(slot));
     tmem = uniform(tmem);
+    // The weights' first two stages on their way to L2 while the kernel that makes the activations ends (one
+    // token quantised and 28672 x 8192: 25.5 -> 25.0 us in all; with five stages the product alone loses up
+    // to 0.6 us to asking twice).
+    if (warp == 0 && elect_one())
+        for (int it = 0; it < min(steps, 2); ++it) {
+            const int k = k0 + it;
+            prefetch_2d(&b_map, 128 * k, n0);
+            prefetch_bulk(a.b_scales + (int64_t(n0 / 128) * a.scale_tiles + int64_t(k) * G::kScaleTiles) * 512,
+                          512 * min(G::kScaleTiles, a.scale_tiles - k * G::kScaleTiles));
+        }
+    __syncwarp();
     ms::wait_for_stream();
 
     bool ok = true;
@@ -202,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
     }
     fence_before();
     __syncwarp();
-    cluster_sync();
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
     const int c0 = NT * int(rank) / int(ranks), c1 = NT * (int(rank) + 1) / int(ranks);
     const int64_t col = int64_t(n0) + 4 * lane;
     const int n = int(max(int64_t(0), min(int64_t(4), a.cols - col)));
@@ -223,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
         if (ok && n > 0) store4(a, int64_t(m0) + c, col, n, v);
     }
     __syncwarp();
-    cluster_sync();  // no CTA leaves while another reads its sums
+    if (ranks > 1) cluster_sync();  // no CTA leaves while another reads its sums
+    else __syncthreads();
     fence_after();
     if (!ok) atomicOr(&ep_op_status_word, 1u);
     if (warp == 2) tmem_free(tmem, G::kColumns);
