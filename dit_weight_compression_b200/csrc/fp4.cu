@@ -20,6 +20,10 @@ constexpr int kPassRows = kThreads / (kTileCols / 8);  // dequantising: 16 threa
 constexpr int kPasses = kTileRows / kPassRows;
 constexpr int kMaxPartials = EP_FP4_SCALE_FLOATS - 1;
 
+// How the rows of a dense matrix lie: 16-byte aligned and whole (in sixteens, or eights when written); at
+// least 8-byte aligned; anywhere.
+enum Rows { kWhole, kEven, kAnywhere };
+
 struct QuantArgs {
     const void* x;
     int64_t stride, rows, cols;
@@ -33,6 +37,7 @@ struct QuantArgs {
     int partials;     // > 0: its maxima are in tensor_scale[1 ..]; 0 and no fixed scale: each block
                       // looks at all of x
     int width;        // alignment of the rows for load_raw8
+    int start_width;  // and of the first element
     bool backwards;   // take the last rows first
 };
 
@@ -64,9 +69,10 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* smem) {
 template <int DT>
 __device__ __forceinline__ uint32_t max_of_chunks(const QuantArgs& a, int64_t first, int64_t step) {
     using T = typename Elem<DT>::T;
-    const int64_t per_row = (a.cols + 7) / 8, n = a.rows * per_row;
     const T* x = static_cast<const T*>(a.x);
-    const bool flat = a.stride == a.cols && a.cols % 8 == 0;  // rows without gaps need no division
+    const bool flat = a.stride == a.cols;  // rows without gaps are one row
+    const int64_t per_row = ((flat ? a.rows * a.cols : a.cols) + 7) / 8, n = (flat ? 1 : a.rows) * per_row;
+    const int width = flat ? a.start_width : a.width;
     uint32_t m = 0;
     for (int64_t i = first; i < n; i += 4 * step) {
         Raw8<DT> r[4];
@@ -74,8 +80,8 @@ __device__ __forceinline__ uint32_t max_of_chunks(const QuantArgs& a, int64_t fi
         for (int k = 0; k < 4; ++k) {
             const int64_t j = i + k * step;
             const int64_t row = flat || j >= n ? 0 : j / per_row, c = 8 * (j - row * per_row);
-            const int have = j >= n ? 0 : flat ? 8 : int(min(int64_t(8), a.cols - c));
-            r[k] = load_raw8<DT>(x + row * a.stride + c, have, a.width);
+            const int have = j >= n ? 0 : int(min(int64_t(8), (flat ? a.rows * a.cols : a.cols) - c));
+            r[k] = load_raw8<DT>(x + row * a.stride + c, have, width);
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) m = max(m, finite_max8<DT>(r[k]));
@@ -98,14 +104,14 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 4 : 6) amax_kernel(co
 // writes their codes and its scale tiles.  A thread has 16 neighbours of 16-bit elements (with 8, a scale
 // was formed 2 or 4 times over and issue took as long as the memory: 100 instructions for 8 elements and
 // 73 us for 8192 x 16384 bf16; now 58 and 60), but 8 of fp32 (16 are 64 bytes, too far from one thread
-// to the next: 40 us for 4096 x 11008, 36 with 8).  FAST: rows in whole sixteens, 16-byte aligned.
-template <int DT, bool NV, bool FAST>
+// to the next: 40 us for 4096 x 11008, 36 with 8).
+template <int DT, bool NV, int ROWS>
 __global__ void __launch_bounds__(kThreads, NV && DT == EP_F32 ? 3 : 4) quantize_kernel(const __grid_constant__ QuantArgs a) {
     using T = typename Elem<DT>::T;
     constexpr int kC = DT == EP_F32 ? 1 : 2;                        // chunks of 8 elements a thread
     constexpr int kParts = kTileCols / (8 * kC);                    // threads a row
     constexpr int kRows = kThreads / kParts, kSteps = kTileRows / kRows;
-    constexpr int kBatch = 4;                                       // steps in flight
+    constexpr int kBatch = ROWS != kAnywhere ? 4 : 2;                            // steps in flight
     constexpr int kOwners = (NV ? 16 : 32) / (8 * kC);              // threads of a scale block
     __shared__ uint32_t red[kThreads / 32];
     __shared__ __align__(16) uint8_t sc[NV ? 1024 : 512];
@@ -123,17 +129,22 @@ __global__ void __launch_bounds__(kThreads, NV && DT == EP_F32 ? 3 : 4) quantize
     const int k = part / kOwners;  // the scale block's column in this tile
 
     float g = 1.0f, g_inv = 1.0f;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(a.x), hi = lo + size_t((a.rows - 1) * a.stride + a.cols) * sizeof(T);
     Raw8<DT> v[kBatch][kC];
 #pragma unroll
     for (int p0 = 0; p0 < kSteps; p0 += kBatch) {
+        Piece<DT> piece[ROWS == kAnywhere ? kBatch : 1];
 #pragma unroll
         for (int p = 0; p < kBatch; ++p) {
             const T* src = x + int64_t(p0 + p) * kRows * a.stride;
-            const bool in = sub + (p0 + p) * kRows < rows;
+            const int have = sub + (p0 + p) * kRows < rows ? n : 0;
+            if constexpr (ROWS != kAnywhere) {
 #pragma unroll
-            for (int c = 0; c < kC; ++c)
-                v[p][c] = FAST ? load_raw8<DT>(src + 8 * c, in && n ? 8 : 0, 16)
-                               : load_raw8<DT>(src + 8 * c, in ? min(n - 8 * c, 8) : 0, a.width);
+                for (int c = 0; c < kC; ++c)
+                    v[p][c] = ROWS == kWhole ? load_raw8<DT>(src + 8 * c, have ? 8 : 0, 16) : load_raw8<DT>(src + 8 * c, min(have - 8 * c, 8), 8);
+            } else {
+                piece[p].load(src, have, lo, hi);
+            }
         }
         if (NV && p0 == 0) {
             if (a.fixed > 0.0f) {
@@ -150,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, NV && DT == EP_F32 ? 3 : 4) quantize
 #pragma unroll
         for (int p = 0; p < kBatch; ++p) {
             const bool in = sub + (p0 + p) * kRows < rows;
+            if constexpr (ROWS == kAnywhere) piece[p].take(x + int64_t(p0 + p) * kRows * a.stride, in ? n : 0, v[p]);
             uint32_t m = abs_max8<DT>(v[p][0]);
             if constexpr (kC == 2) m = max(m, abs_max8<DT>(v[p][1]));
             const Block b = block_scale<DT, NV>(lanes_max<kOwners>(m), g, g_inv);
@@ -185,14 +197,17 @@ struct DequantArgs {
     void* out;
     int64_t stride, rows, cols, row_bytes;
     int col_tiles, scale_tiles;
-    int width;        // alignment of out's rows for store8
+    int rows_lie;     // Rows
 };
 
 // The same blocks backwards: scale tiles to shared memory, 4 bytes of codes a thread, 8 elements out.
-template <int DT, bool NV>
-__global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs a) {
+// Rows anywhere go through shared memory, so that the lanes of a warp store neighbouring elements, or pairs
+// of them (5230 x 10463 bf16: 35 us; 8 neighbours a lane, one by one, took several times that).
+template <int DT, bool NV, int ROWS>
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const __grid_constant__ DequantArgs a) {
     using T = typename Elem<DT>::T;
     __shared__ __align__(16) uint8_t sc[NV ? 1024 : 512];
+    __shared__ __align__(16) T staged[ROWS == kAnywhere ? kPassRows * kTileCols : 8];
     wait_for_stream();
     const int64_t row0 = int64_t(blockIdx.x / a.col_tiles) * kTileRows;
     const int64_t col = int64_t(blockIdx.x % a.col_tiles) * kTileCols + 8 * (threadIdx.x % 16);
@@ -211,20 +226,45 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
         codes[p] = col_in && r < a.rows ? *reinterpret_cast<const uint32_t*>(a.data + r * a.row_bytes + col / 2) : 0;
     }
     __syncthreads();
-    if (!col_in) return;
-    const int n = int(min(int64_t(8), a.cols - col));
+    const int64_t tile0 = col - 8 * (threadIdx.x % 16);
+    const int n = int(min(int64_t(kTileCols), a.cols - tile0));  // columns of this tile
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
         const int r = sub + p * kPassRows;
-        if (row0 + r >= a.rows) break;
         const int k = (threadIdx.x % 16) / (NV ? 2 : 4);
         const float s = scale_value<NV>(sc[(k / 4) * 512 + 16 * (r % 32) + 4 * (r / 32) + k % 4]);
         float v[8];
         e2m1_values8(codes[p], v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = v[j] * s * g;
-        T* dst = static_cast<T*>(a.out) + (row0 + r) * a.stride + col;
-        store8<DT>(dst, n, a.width, v);
+        T* row = static_cast<T*>(a.out) + (row0 + r) * a.stride + tile0;
+        if constexpr (ROWS != kAnywhere) {
+            if (row0 + r < a.rows && col_in)
+                store8<DT>(row + 8 * (threadIdx.x % 16), ROWS == kWhole ? 8 : min(8, n - 8 * int(threadIdx.x % 16)), ROWS == kWhole ? 16 : 8, v);
+        } else {
+            // the warp's two rows, one after the other
+            store8<DT>(staged + sub * kTileCols + 8 * (threadIdx.x % 16), 8, 16, v);
+            __syncwarp();
+            const int lane = threadIdx.x % 32, first = r - sub % 2;
+            row -= (sub % 2) * a.stride;
+#pragma unroll
+            for (int q = 0; q < 2; ++q, row += a.stride) {
+                if (row0 + first + q >= a.rows) break;
+                const T* from = staged + (sub - sub % 2 + q) * kTileCols;
+                if (sizeof(T) == 2 && reinterpret_cast<uintptr_t>(row) % 4 == 0) {
+#pragma unroll
+                    for (int e = 2 * lane; e < kTileCols; e += 64) {
+                        if (e + 1 < n) *reinterpret_cast<uint32_t*>(row + e) = *reinterpret_cast<const uint32_t*>(from + e);
+                        else if (e < n) row[e] = from[e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = lane; e < kTileCols; e += 32)
+                        if (e < n) row[e] = from[e];
+                }
+            }
+            __syncwarp();
+        }
     }
 }
 
@@ -234,15 +274,18 @@ cudaError_t launch_quantize(const QuantArgs& q, bool nv, int64_t grid, int amax_
         cudaError_t e = op::launch(amax_kernel<DT>, dim3(unsigned(amax_grid)), dim3(kThreads), 0, st, q);
         if (e != cudaSuccess) return e;
     }
-    const bool fast = q.width == 16 && q.cols % 16 == 0;
-    const auto kernel = nv ? (fast ? quantize_kernel<DT, true, true> : quantize_kernel<DT, true, false>)
-                           : (fast ? quantize_kernel<DT, false, true> : quantize_kernel<DT, false, false>);
+    const int rows = q.width == 16 && q.cols % 16 == 0 ? kWhole : q.width >= 8 ? kEven : kAnywhere;
+    const auto kernel = rows == kWhole  ? (nv ? quantize_kernel<DT, true, kWhole> : quantize_kernel<DT, false, kWhole>)
+                        : rows == kEven ? (nv ? quantize_kernel<DT, true, kEven> : quantize_kernel<DT, false, kEven>)
+                                        : (nv ? quantize_kernel<DT, true, kAnywhere> : quantize_kernel<DT, false, kAnywhere>);
     return op::launch(kernel, dim3(unsigned(grid)), dim3(kThreads), 0, st, q);
 }
 template <int DT>
 cudaError_t launch_dequantize(const DequantArgs& q, bool nv, int64_t grid, cudaStream_t st) {
-    return op::launch(nv ? dequantize_kernel<DT, true> : dequantize_kernel<DT, false>, dim3(unsigned(grid)),
-                      dim3(kThreads), 0, st, q);
+    const auto kernel = q.rows_lie == kWhole  ? (nv ? dequantize_kernel<DT, true, kWhole> : dequantize_kernel<DT, false, kWhole>)
+                        : q.rows_lie == kEven ? (nv ? dequantize_kernel<DT, true, kEven> : dequantize_kernel<DT, false, kEven>)
+                                              : (nv ? dequantize_kernel<DT, true, kAnywhere> : dequantize_kernel<DT, false, kAnywhere>);
+    return op::launch(kernel, dim3(unsigned(grid)), dim3(kThreads), 0, st, q);
 }
 
 // Tensors of at most this many bytes are searched for their largest value by every block itself
@@ -310,6 +353,7 @@ int quantize(const ep_tensor* x, const ep_fp4_tensor* out, double tensor_scale, 
         q.scale_tiles = int(op::div_up(op::fp4_blocks(out->format, x->cols), 4));
         q.fixed = float(tensor_scale);
         q.width = op::access_width(x->data, x->row_stride * es);
+        q.start_width = op::access_width(x->data, 0);
         const int64_t grid = op::div_up(x->rows, kTileRows) * q.col_tiles;
         if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, std::string(who) + ": the matrix is too large");
         int amax_grid = 0;
@@ -378,7 +422,8 @@ extern "C" int ep_fp4_dequantize(const ep_fp4_tensor* x, const ep_tensor* out, v
     q.row_bytes = op::fp4_row_bytes(x->cols);
     q.col_tiles = int(op::div_up(x->cols, kTileCols));
     q.scale_tiles = int(op::div_up(op::fp4_blocks(x->format, x->cols), 4));
-    q.width = op::access_width(out->data, out->row_stride * op::elem_bytes(out->dtype));
+    const int width = op::access_width(out->data, out->row_stride * op::elem_bytes(out->dtype));
+    q.rows_lie = width == 16 && x->cols % 8 == 0 ? kWhole : width >= 8 ? kEven : kAnywhere;
     const int64_t grid = op::div_up(x->rows, kTileRows) * q.col_tiles;
     if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_dequantize: the tensor is too large");
     const bool nv = x->format == EP_NVFP4;

@@ -90,6 +90,55 @@ __device__ __forceinline__ Raw8<DT> load_raw8(const typename Elem<DT>::T* p, int
     return r;
 }
 
+// 32 bytes of elements (16 or 8) at any address: the aligned 16-byte granules that hold them, all loaded
+// before the first is used, and then shifted into place.  Nothing outside [lo, hi), the matrix from its
+// first element to its last, is read: a granule that reaches over either end goes element by element.
+template <int DT>
+__device__ __noinline__ uint4 load_granule_parts(uintptr_t at, uintptr_t lo, uintptr_t hi) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    constexpr int kSize = sizeof(typename Elem<DT>::T);
+#pragma unroll
+    for (int b = 0; b < 16; b += kSize)
+        if (at + b >= lo && at + b < hi) {
+            if constexpr (kSize == 4) w[b / 4] = *reinterpret_cast<const uint32_t*>(at + b);
+            else w[b / 4] |= uint32_t(*reinterpret_cast<const uint16_t*>(at + b)) << (8 * (b % 4));
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int DT>
+struct Piece {
+    uint32_t w[12];
+    // n: elements wanted, 0 to 32 / size.
+    __device__ __forceinline__ void load(const typename Elem<DT>::T* p, int n, uintptr_t lo, uintptr_t hi) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p), first = at & ~uintptr_t(15);
+        const uintptr_t end = n > 0 ? at + n * sizeof(*p) : first;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            const uintptr_t g = first + 16 * i;
+            if (g < end) u = g >= lo && g + 16 <= hi ? *reinterpret_cast<const uint4*>(g) : load_granule_parts<DT>(g, lo, hi);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+    }
+    // The elements, zeros from the n-th on, as chunks of 8.
+    __device__ __forceinline__ void take(const typename Elem<DT>::T* p, int n, Raw8<DT>* v) {
+        const uint32_t s = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
+#pragma unroll
+        for (int i = 0; i < 10; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 9; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
+        if constexpr (DT != EP_F32)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = s & 2 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+        constexpr int kWords = DT == EP_F32 ? 8 : 4, kPer = DT == EP_F32 ? 1 : 2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t keep = n >= kPer * (i + 1) ? 0xffffffffu : kPer == 2 && n == 2 * i + 1 ? 0xffffu : 0u;
+            v[i / kWords].w[i % kWords] = w[i] & keep;
+        }
+    }
+};
+
 // Elements 2i and 2i + 1 as floats.
 template <int DT>
 __device__ __forceinline__ float2 pair(const Raw8<DT>& r, int i) {
@@ -284,16 +333,23 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
+// Eight values as they are stored.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> pack8(const float* v) {
+    Raw8<DT> r;
+#pragma unroll
+    for (int i = 0; i < (DT == EP_F32 ? 8 : 4); ++i) {
+        if constexpr (DT == EP_F32) r.w[i] = __float_as_uint(v[i]);
+        else r.w[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
+    }
+    return r;
+}
 // The first n of eight values to p, which is aligned to `width` bytes as for load_raw8.
 template <int DT>
 __device__ __forceinline__ void store8(typename Elem<DT>::T* p, int n, int width, const float* v) {
     constexpr int W = DT == EP_F32 ? 8 : 4;
-    uint32_t w[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        if constexpr (DT == EP_F32) w[i] = __float_as_uint(v[i]);
-        else w[i] = pack2<DT>(v[2 * i], v[2 * i + 1]);
-    }
+    const Raw8<DT> packed = pack8<DT>(v);
+    const uint32_t* w = packed.w;
     if (n == 8 && width == 16) {
 #pragma unroll
         for (int i = 0; i < W / 4; ++i)
