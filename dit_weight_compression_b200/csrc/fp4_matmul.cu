@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
             v[3] += f.w;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = v[j] * alpha + bias[j];
+        for (int j = 0; j < 4; ++j) v[j] = __fmaf_rn(v[j], alpha, bias[j]);
         if (ok && n > 0) store4(a, int64_t(m0) + c, col, n, v);
     }
     __syncwarp();
@@ -447,11 +447,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
             if (lane == 0) bar_arrive_cluster(first_cta(taken));
             const int64_t row0 = int64_t(256) * ta + 128 * int(rank) + 32 * quarter, col = int64_t(256) * tb + 128 * half;
             const uint32_t buf = out_bufs + (warp - 2) * G::kOut;
-            if (m.bias) {
+            if (m.bias) {  // the warp's 128 columns', through its buffer
+                __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 128; ++c) {
-                    const float v = __uint_as_float(r[c / 16][c % 16]) * alpha + (col + c < m.cols ? bias_at(m, col + c) : 0.0f);
-                    r[c / 16][c % 16] = __float_as_uint(v);
+                for (int j = 0; j < 4; ++j) {
+                    const int c = 32 * j + lane;
+                    const float v = col + c < m.cols ? bias_at(m, col + c) : 0.0f;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + 4 * c), "f"(v) : "memory");
+                }
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 128; c += 4) {
+                    float v[4];
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                                 : "r"(buf + 4 * c));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        r[c / 16][c % 16 + j] = __float_as_uint(__fmaf_rn(__uint_as_float(r[c / 16][c % 16 + j]), alpha, v[j]));
                 }
             } else {
 #pragma unroll
@@ -605,21 +618,29 @@ int run_pairs(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& 
     return EP_OK;
 }
 
+// CTAs of one tile: the most whose clusters all fit the device at once, with four stages each.  (4096
+// outputs of 4096 for one token: 5.4 us with 4, 6.5 with 8 of two stages; 300 tokens: 11.1 us with 2, 16.7
+// with 3, which need a second round.)
 template <int NT, bool NV>
-int run_split(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int dev, cudaStream_t st) {
-    using G = Geo<NT, NV>;
-    CUtensorMap b_map, a_map;
-    if (!operand_map(&b_map, b, 128) || !operand_map(&a_map, a, NT)) return set_error(EP_ERR_CUDA, "ep_fp4_matmul: tensor map");
-    // CTAs of one tile: the most whose clusters all fit the device at once, with four stages each.  (4096
-    // outputs of 4096 for one token: 5.4 us with 4, 6.5 with 8 of two stages; 300 tokens: 11.1 us with 2,
-    // 16.7 with 3, which need a second round.)
-    const int64_t tiles = int64_t(args.n_tiles) * op::div_up(a->rows, NT);
-    int split = std::min(kMaxSplit, (args.steps + 3) / 4), clusters = 0;
+cudaError_t split_of(int dev, int64_t tiles, int steps, int& split) {
+    int clusters = 0;
+    split = std::min(kMaxSplit, (steps + 3) / 4);
     cudaError_t e = clusters_of<NT, NV>(dev, 1, clusters);
     for (; e == cudaSuccess && split > 1; --split) {
         e = clusters_of<NT, NV>(dev, split, clusters);
         if (tiles <= clusters) break;
     }
+    return e;
+}
+
+template <int NT, bool NV>
+int run_split(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int dev, cudaStream_t st) {
+    using G = Geo<NT, NV>;
+    CUtensorMap b_map, a_map;
+    if (!operand_map(&b_map, b, 128) || !operand_map(&a_map, a, NT)) return set_error(EP_ERR_CUDA, "ep_fp4_matmul: tensor map");
+    const int64_t tiles = int64_t(args.n_tiles) * op::div_up(a->rows, NT);
+    int split = 1;
+    cudaError_t e = split_of<NT, NV>(dev, tiles, args.steps, split);
     const int64_t grid = tiles * split;
     if (grid > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: too many tiles");
     if (e == cudaSuccess) {
@@ -635,9 +656,16 @@ int matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& arg
     if (m <= 16) return run_split<16, NV>(a, b, args, dev, st);
     if (m <= 32) return run_split<32, NV>(a, b, args, dev, st);
     if (m <= 64) return run_split<64, NV>(a, b, args, dev, st);
-    if (m <= 128) return run_split<128, NV>(a, b, args, dev, st);
-    // (130 tokens, 8192 outputs of 28672: 41 us in pairs, 51 split; 300, 4096 of 4096: 10.8 and 12.3; only
-    // where 256 tokens meet fewer outputs than 4096 split is ahead, 9.2 against 10.4.)
+    // More than 128 tokens go in pairs, unless there are so few outputs that each tile's sum along K is
+    // worth sharing among three CTAs or more (200 tokens, 2048 outputs of 8192: 7.7 us so, 14.1 in pairs;
+    // 256, 4096 of 4096: 8.9 and 9.8; 384, which can share by two only: 10.5 and 10.0; 130, 28672 of 1024:
+    // 13.9 and 10.1).
+    int split = kMaxSplit;
+    if (m > 128) {
+        const cudaError_t e = split_of<128, NV>(dev, int64_t(args.n_tiles) * op::div_up(m, 128), args.steps, split);
+        if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_matmul: ") + cudaGetErrorString(e));
+    }
+    if (split >= 3) return run_split<128, NV>(a, b, args, dev, st);
     return run_pairs<NV>(a, b, args, dev, st);
 }
 

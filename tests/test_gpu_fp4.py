@@ -219,7 +219,8 @@ def random_fp4(ep, rows, cols, fmt, seed, plain):
 
 MATMULS = [(1, 1, 1), (1, 128, 256), (1, 300, 64), (2, 129, 65), (7, 40, 4096), (16, 257, 500), (17, 1000, 1024), (33, 128, 2048),
            (64, 513, 100), (65, 130, 333), (100, 100, 100), (128, 2, 3000), (129, 64, 64), (130, 300, 1111), (256, 256, 256),
-           (300, 700, 1500), (520, 1030, 4096), (2100, 130, 320), (1, 5000, 4000), (3000, 4200, 96), (2500, 2600, 700)]
+           (300, 700, 1500), (520, 1030, 4096), (2100, 130, 320), (1, 5000, 4000), (3000, 4200, 96), (2500, 2600, 700), (1000, 512, 4096),
+           (140, 20000, 128), (257, 255, 4095)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
