@@ -14,8 +14,8 @@ using namespace ms;
 
 // Two variants of each kernel.  The common one serves rows of up to 256 elements in whole eights, 16-byte
 // aligned outside the cache: a lane has 16 elements, so that the row's addresses, maximum and scale, which
-// cost as much as 8 elements, are shared by more (per 8 elements and lane 228 -> 112 instructions in an
-// int8 write, 120 -> 61 in an fp8 read, of the 133 that copying at the memory's rate leaves time for).
+// cost as much as 8 elements, are shared by more (for 8 elements 228 -> 130 instructions of a lane in an
+// int8 write, 138 -> 73 in an fp8 read; copying at the memory's rate leaves time for 133).
 // The other serves every head up to 1024 elements, 8 a lane, at any alignment.
 constexpr int kThreads = 256;
 constexpr int kMaxHeadDim = 1024;

@@ -65,26 +65,30 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* smem) {
     return lanes_max<kThreads / 32>(smem[threadIdx.x % (kThreads / 32)]);
 }
 
-// Chunks of eight elements `first`, `first + step`, ... of x, row by row; four in flight.
+// The largest finite |v| of chunks of eight elements `first`, `first + step`, ... of x; four in flight.
 template <int DT>
 __device__ __forceinline__ uint32_t max_of_chunks(const QuantArgs& a, int64_t first, int64_t step) {
     using T = typename Elem<DT>::T;
     const T* x = static_cast<const T*>(a.x);
     const bool flat = a.stride == a.cols;  // rows without gaps are one row
-    const int64_t per_row = ((flat ? a.rows * a.cols : a.cols) + 7) / 8, n = (flat ? 1 : a.rows) * per_row;
+    const int64_t cols = flat ? a.rows * a.cols : a.cols, per_row = (cols + 7) / 8, n = (flat ? 1 : a.rows) * per_row;
     const int width = flat ? a.start_width : a.width;
     uint32_t m = 0;
-    for (int64_t i = first; i < n; i += 4 * step) {
-        Raw8<DT> r[4];
+    int64_t i = first;
+    if (flat && width == 16) {  // whole chunks: nothing to check, nothing to divide
+        const int64_t whole = cols / 8;
+        const T* p = x + 8 * first;
+        for (; i + 3 * step < whole; i += 4 * step, p += 32 * step) {
+            Raw8<DT> r[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t j = i + k * step;
-            const int64_t row = flat || j >= n ? 0 : j / per_row, c = 8 * (j - row * per_row);
-            const int have = j >= n ? 0 : int(min(int64_t(8), (flat ? a.rows * a.cols : a.cols) - c));
-            r[k] = load_raw8<DT>(x + row * a.stride + c, have, width);
+            for (int k = 0; k < 4; ++k) r[k] = load_raw8<DT>(p + 8 * k * step, 8, 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m = max(m, finite_max8<DT>(r[k]));
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m = max(m, finite_max8<DT>(r[k]));
+    }
+    for (; i < n; i += step) {
+        const int64_t row = flat ? 0 : i / per_row, c = 8 * (i - row * per_row);
+        m = max(m, finite_max8<DT>(load_raw8<DT>(x + row * a.stride + c, int(min(int64_t(8), cols - c)), width)));
     }
     return m;
 }
@@ -103,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 4 : 6) amax_kernel(co
 // One pass: a block reads its 128 x 128 elements, forms the block scales among neighbouring threads and
 // writes their codes and its scale tiles.  A thread has 16 neighbours of 16-bit elements (with 8, a scale
 // was formed 2 or 4 times over and issue took as long as the memory: 100 instructions for 8 elements and
-// 73 us for 8192 x 16384 bf16; now 58 and 60), but 8 of fp32 (16 are 64 bytes, too far from one thread
+// 73 us for 8192 x 16384 bf16; now 65 and 52), but 8 of fp32 (16 are 64 bytes, too far from one thread
 // to the next: 40 us for 4096 x 11008, 36 with 8).
 template <int DT, bool NV, int ROWS>
 __global__ void __launch_bounds__(kThreads, NV && DT == EP_F32 ? 3 : 4) quantize_kernel(const __grid_constant__ QuantArgs a) {
