@@ -156,7 +156,8 @@ class FP4Tensor:
             i, j = t._scale_tiles
             s = torch.zeros(i * 128, j * 4, dtype=torch.uint8, device=dev)
             s[:rows, :blocks] = scale_rows if format == "mxfp4" else scale_rows & 0x7F  # E4M3 scales have no sign
-            t.scales.copy_(s.view(i, 4, 32, j, 4).permute(0, 3, 2, 1, 4).reshape(-1))
+            # four scales of a row at a time: tiles of 32 x 4 words
+            t.scales.view(torch.int32).view(i, j, 32, 4).copy_(s.view(torch.int32).view(i, 4, 32, j).permute(0, 3, 2, 1))
             t.tensor_scale.copy_(tensor_scale.reshape(1))
         return t
 
