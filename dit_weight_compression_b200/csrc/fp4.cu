@@ -97,10 +97,27 @@ __device__ __forceinline__ uint32_t max_of_chunks(const QuantArgs& a, int64_t fi
 // (5.6 TB/s of 8192 x 11008 bf16).
 template <int DT>
 __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 4 : 6) amax_kernel(const QuantArgs a) {
+    using T = typename Elem<DT>::T;
     __shared__ uint32_t smem[kThreads / 32];
     wait_for_stream();
-    const uint32_t m = block_max(
-        max_of_chunks<DT>(a, int64_t(blockIdx.x) * kThreads + threadIdx.x, int64_t(gridDim.x) * kThreads), smem);
+    uint32_t m = 0;
+    if (a.stride == a.cols) {
+        m = max_of_chunks<DT>(a, int64_t(blockIdx.x) * kThreads + threadIdx.x, int64_t(gridDim.x) * kThreads);
+    } else {  // rows apart: runs of a row, so that a division serves four loads of the block
+        constexpr int kRun = 4 * 8 * kThreads;
+        const int64_t runs = (a.cols + kRun - 1) / kRun;
+        for (int64_t u = blockIdx.x; u < a.rows * runs; u += gridDim.x) {
+            const int64_t row = u / runs, c = (u - row * runs) * kRun + 8 * int(threadIdx.x);
+            const T* p = static_cast<const T*>(a.x) + row * a.stride + c;
+            Raw8<DT> r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                r[k] = load_raw8<DT>(p + 8 * k * kThreads, int(max(int64_t(0), min(int64_t(8), a.cols - c - 8 * k * kThreads))), a.width);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m = max(m, finite_max8<DT>(r[k]));
+        }
+    }
+    m = block_max(m, smem);
     if (threadIdx.x == 0) a.tensor_scale[1 + blockIdx.x] = abs_value<DT>(m);
 }
 

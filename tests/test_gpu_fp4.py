@@ -149,6 +149,18 @@ def test_strides_and_alignment(ep, fmt, off, stride, dtype):
     assert torch.equal(out.double().cpu(), want)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("off", [0, 5, 8])
+def test_long_rows_apart(ep, dtype, off):
+    """Rows of several runs of the maximum's own pass, with gaps between them; the largest value is the last."""
+    big = sample(6, 20011, dtype, 8)
+    x = big[:, off:off + 20000]
+    x[5, 19999] = 3e4
+    check_quantized(ep, ep.fp4_quantize(x, "nvfp4"), x)
+    y = x.contiguous()
+    assert torch.equal(ep.fp4_quantize(y, "nvfp4").data, ep.fp4_quantize(x, "nvfp4").data)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("shape", [(1, 1), (3, 47), (129, 257), (200, 640)])
@@ -361,6 +373,23 @@ def test_streams_and_graphs(ep):
         d = ep.fp4_dequantize(q, stream=st)
         s.synchronize()
         assert torch.equal(y, want[1]) and torch.equal(d, ep.fp4_dequantize(q))
+    ep.op_status()
+
+
+def test_products_side_by_side(ep):
+    """Products of every kind on four streams at once, sharing weights: each as if it were alone."""
+    w = ep.fp4_quantize(sample(3000, 2048, torch.bfloat16, 40), "nvfp4")
+    xs = [ep.fp4_quantize(sample(m, 2048, torch.bfloat16, 41 + m), "nvfp4") for m in (1, 60, 300, 2100)]
+    want = [ep.fp4_matmul(x, w) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for x, s in zip(xs, streams):
+            got.append(ep.fp4_matmul(x, w, stream=s))
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 4])
     ep.op_status()
 
 
