@@ -184,7 +184,7 @@ __device__ __forceinline__ void find_slots(const WriteArgs& a, int64_t t0, int n
     __syncthreads();
 }
 
-// A block takes a few tokens, all heads of all caches; rows go in batches of LANES lanes a row, whose loads
+// A block takes a few tokens, all heads of one cache; rows go in batches of LANES lanes a row, whose loads
 // are all on their way before the first is used, those of the first batch before the slots are looked up.
 template <int DT, int FMT, int LANES>
 __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_kernel(const __grid_constant__ WriteArgs a) {
@@ -196,7 +196,9 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
     wait_for_stream();
     const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
     const int n = int(min(int64_t(a.per_block), a.tokens - t0));
-    const int rows = n * a.heads, all = a.n * rows;
+    const CacheView& c = a.c[blockIdx.y];
+    const int rows = n * a.heads;
+    const T* src = static_cast<const T*>(c.heads) + t0 * c.token_stride;
     const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     // 4-bit: sixteen neighbours, of one block; 8-bit: twice eight, so that lanes touch neighbouring bytes
     const int e = (kFp4 ? 16 : 8) * lane, e2 = e + (kFp4 ? 8 : 8 * LANES);
@@ -204,13 +206,9 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
     auto load = [&](int base) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            int r = base + u * kStep + sub;
-            const int ci = r >= rows ? 1 : 0;
-            r -= ci ? rows : 0;
-            const int i = quotient(r, a.heads_inv), h = r - i * a.heads;
-            const CacheView& c = a.c[ci];
-            const bool in = base + u * kStep + sub < all;
-            const T* p = static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride;
+            const int r = base + u * kStep + sub, i = quotient(r, a.heads_inv), h = r - i * a.heads;
+            const bool in = r < rows;
+            const T* p = src + i * c.token_stride + h * c.head_stride;
             v[u][0] = load_raw8<DT>(p + e, in && e < c.head_dim ? 8 : 0, 16);
             v[u][1] = load_raw8<DT>(p + e2, in && e2 < c.head_dim ? 8 : 0, 16);
         }
@@ -218,16 +216,13 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
     load(0);
     find_slots(a, t0, n, slot, dropped);
     // every lane of a warp stays in the loop: rows past the end are zeros and not written
-    for (int base = 0; base < all;) {
+    for (int base = 0; base < rows;) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            if (base + u * kStep >= all) break;
-            int r = base + u * kStep + sub;
-            const bool in = r < all;
-            const int ci = r >= rows ? 1 : 0;
-            r -= ci ? rows : 0;
+            if (base + u * kStep >= rows) break;
+            const int r = base + u * kStep + sub;
+            const bool in = r < rows;
             const int i = in ? quotient(r, a.heads_inv) : 0, h = r - i * a.heads;
-            const CacheView& c = a.c[ci];
             const int64_t to = in ? slot[i] : -1, row = to * a.heads + h;
             const bool live = to >= 0 && e < c.head_dim;
             uint32_t bits = max(abs_max8<DT>(v[u][0]), abs_max8<DT>(v[u][1]));
@@ -253,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, DT == EP_F32 ? 3 : 4) cache_write_ke
             }
         }
         base += kBatch * kStep;
-        if (base < all) load(base);
+        if (base < rows) load(base);
     }
 }
 
@@ -311,10 +306,9 @@ __global__ void __launch_bounds__(kThreads) cache_write_any_kernel(const __grid_
     const int64_t t0 = int64_t(blockIdx.x) * a.per_block;
     const int n = int(min(int64_t(a.per_block), a.tokens - t0));
     find_slots(a, t0, n, slot, dropped);
-    const int rows = n * a.heads;
-    for (int r = threadIdx.x / 32; r < a.n * rows; r += kThreads / 32) {
-        const int ci = r >= rows, i = quotient(r - ci * rows, a.heads_inv), h = r - ci * rows - i * a.heads;
-        const CacheView& c = a.c[ci];
+    const CacheView& c = a.c[blockIdx.y];
+    for (int r = threadIdx.x / 32; r < n * a.heads; r += kThreads / 32) {
+        const int i = quotient(r, a.heads_inv), h = r - i * a.heads;
         if (slot[i] >= 0)
             write_any_row<DT, FMT>(c, static_cast<const T*>(c.heads) + (t0 + i) * c.token_stride + h * c.head_stride,
                                    slot[i] * a.heads + h);
@@ -667,10 +661,10 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
             part.c[i].heads = static_cast<uint8_t*>(w.c[i].heads) + t0 * w.c[i].token_stride * es;
         // a block's rows are one batch of its threads (16384 tokens of 8 heads of 128, int8: 27 us with 8
         // tokens a block, 30 with 16); few tokens are spread over the SMs
-        const int batch = 4 * kThreads / std::max(lanes, 4) / (w.heads * n);
+        const int batch = 4 * kThreads / std::max(lanes, 4) / w.heads;
         part.per_block = int(std::max<int64_t>(1, std::min<int64_t>({kMaxWriteTokens, batch, op::div_up(part.tokens, 4 * sms)})));
         part.alone = part.tokens <= kAloneTokens;
-        const dim3 grid(unsigned(op::div_up(part.tokens, part.per_block)));
+        const dim3 grid(unsigned(op::div_up(part.tokens, part.per_block)), unsigned(n));
         const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, lanes, grid, st)
                               : src[0].dtype == EP_FP16 ? write_as<EP_FP16>(caches[0].format, part, lanes, grid, st)
                                                         : write_as<EP_F32>(caches[0].format, part, lanes, grid, st);
