@@ -21,7 +21,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxHeadDim = 1024;
 constexpr int kMaxFastDim = 256;
 constexpr int kLaunchTokens = 65536; // tokens of one write launch
-constexpr int kMaxWriteTokens = 16;  // most tokens of one block of a write
+constexpr int kMaxWriteTokens = 64;  // most tokens of one block of a write
 constexpr int kAloneTokens = 1024;   // up to so many tokens a write looks for repeated slots itself
 constexpr int kMendThreads = 1024;
 constexpr int kMendTokens = 512;     // tokens of one block of mend_kernel
@@ -662,7 +662,7 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
         // a block's rows are one batch of its threads (16384 tokens of 8 heads of 128, int8: 27 us with 8
         // tokens a block, 30 with 16); few tokens are spread over the SMs
         const int batch = 4 * kThreads / std::max(lanes, 4) / w.heads;
-        part.per_block = int(std::max<int64_t>(1, std::min<int64_t>({kMaxWriteTokens, batch, op::div_up(part.tokens, 4 * sms)})));
+        part.per_block = int(std::max<int64_t>(1, std::min<int64_t>({kMaxWriteTokens, batch, op::div_up(part.tokens, 2 * sms)})));
         part.alone = part.tokens <= kAloneTokens;
         const dim3 grid(unsigned(op::div_up(part.tokens, part.per_block)), unsigned(n));
         const cudaError_t e = src[0].dtype == EP_BF16   ? write_as<EP_BF16>(caches[0].format, part, lanes, grid, st)
