@@ -53,13 +53,17 @@ _HERE = _Here()
 _current_device = torch.cuda.current_device
 
 
-def _on(device: torch.device, stream):
-    """(context in which `device` is current and temporaries belong to the call's stream, its handle)."""
+def _on(device: torch.device, stream, *used):
+    """(context in which `device` is current and temporaries belong to the call's stream, its handle).
+    `used`: the tensors of the call, whose memory a stream given by hand then holds on to."""
     index = device.index
     if stream is None:
         return (_HERE if index == _current_device() else torch.cuda.device(device)), _raw_stream(index)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+    for t in used:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
@@ -176,7 +180,7 @@ def fp4_quantize(x: torch.Tensor, format: str = "nvfp4", *, tensor_scale: float 
     `tensor_scale` (nvfp4 only): a power of two, else it is taken from the data in a pass of its own."""
     _cuda(x, "x")
     view = _view(x)
-    ctx, st = _on(x.device, stream)
+    ctx, st = _on(x.device, stream, x, out and out._buffer)
     with ctx:
         out = _made(x.shape, format, x.device, out, "fp4_quantize")
         _check(lib().ep_fp4_quantize(ctypes.byref(view), out._ref, 0.0 if tensor_scale is None else float(tensor_scale), st),
@@ -198,7 +202,7 @@ def _dense(shape, dtype, device, out=None):
 def fp4_dequantize(x: FP4Tensor, *, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
     """The values of a 4-bit tensor as a bf16, fp16 or fp32 tensor (ep_fp4_dequantize)."""
-    ctx, st = _on(x.device, stream)
+    ctx, st = _on(x.device, stream, x._buffer, out)
     with ctx:
         out, view = _dense(x.shape, dtype, x.device, out)
         _check(lib().ep_fp4_dequantize(x._ref, ctypes.byref(view), st), "ep_fp4_dequantize")
@@ -214,7 +218,7 @@ def decompress_fp4(compressed: CompressedTensor, format: str = "nvfp4", *, tenso
         dev = out.device
     elif dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    ctx, st = _on(dev, stream)
+    ctx, st = _on(dev, stream, out and out._buffer)
     with ctx:
         out = _made(compressed.shape, format, dev, out, "decompress_fp4")
         work, view = _dense(compressed.shape, dtype, dev)
@@ -227,7 +231,7 @@ def fp4_matmul(a: FP4Tensor, b: FP4Tensor, *, bias: torch.Tensor | None = None, 
                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """a @ b.T + bias for two 4-bit tensors of one format (ep_fp4_matmul), as bf16, fp16 or fp32.
     `bias` has one element a row of b, of the output's type."""
-    ctx, st = _on(a.device, stream)
+    ctx, st = _on(a.device, stream, a._buffer, b._buffer, bias, out)
     with ctx:
         out, view = _dense((a.shape[0], b.shape[0]), dtype, a.device, out)
         p = None
@@ -319,7 +323,7 @@ def cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
     if slots.dtype != torch.int64 or slots.dim() != 1 or slots.shape[0] != k.shape[0] or not slots.is_contiguous():
         raise ValueError("cache_write: slots must be a contiguous int64 vector with one entry a token")
     views = _TwoHeads(_heads(k, "k"), _heads(v, "v"))
-    ctx, st = _on(cache.device, stream)
+    ctx, st = _on(cache.device, stream, k, v, slots, *cache._pools)
     with ctx:
         _check(lib().ep_cache_write(cache._views, views, 2, slots.data_ptr(), st), "ep_cache_write")
 
@@ -341,7 +345,7 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, cu_seqlens: torch.Tenso
         raise ValueError("cache_read: cu_seqlens must be a contiguous vector of one more entry than there are sequences")
     if out is None and total is None:
         raise ValueError("cache_read: give total or out")
-    ctx, st = _on(cache.device, stream)
+    ctx, st = _on(cache.device, stream, page_table, cu_seqlens, *cache._pools, *(out or ()))
     with ctx:
         if out is None:
             rows, h, d, dev = int(total), cache.heads, cache.head_dim, cache.device

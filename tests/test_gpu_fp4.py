@@ -393,6 +393,29 @@ def test_products_side_by_side(ep):
     ep.op_status()
 
 
+def test_inputs_dropped_while_another_stream_reads_them(ep):
+    """Calls on a stream given by hand hold on to their inputs: the allocator does not hand them out again
+    before that stream is done with them."""
+    s = torch.cuda.Stream()
+    w = ep.fp4_quantize(sample(4096, 4096, torch.bfloat16, 50), "nvfp4")
+    big = ep.fp4_quantize(sample(8192, 4096, torch.bfloat16, 51), "nvfp4")
+    x = sample(2048, 4096, torch.bfloat16, 52)
+    want = ep.fp4_matmul(ep.fp4_quantize(x, "nvfp4"), w)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _ in range(4):
+            ep.fp4_matmul(big, w, stream=s)               # the stream is busy
+        q = ep.fp4_quantize(x, "nvfp4")
+        s.wait_stream(torch.cuda.current_stream())
+        y = ep.fp4_matmul(q, w, stream=s)
+        n = q._buffer.numel()
+        del q
+        for _ in range(8):
+            torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        s.synchronize()
+        assert torch.equal(y, want)
+
+
 def test_first_calls_in_a_capture(ep):
     """A process whose first product of every kind is captured: the look-ups that a first call makes are
     none that a capture forbids."""
