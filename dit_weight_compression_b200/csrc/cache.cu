@@ -659,8 +659,8 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
         part.tokens = std::min<int64_t>(kLaunchTokens, tokens - t0);
         for (int i = 0; i < n; ++i)
             part.c[i].heads = static_cast<uint8_t*>(w.c[i].heads) + t0 * w.c[i].token_stride * es;
-        // a block's rows are one batch of its threads (16384 tokens of 8 heads of 128, int8: 27 us with 8
-        // tokens a block, 30 with 16); few tokens are spread over the SMs
+        // a block's rows are one batch of its threads (16384 tokens of 8 heads of 128, int8: 26.9 us with these 16
+        // tokens a block, 29.8 with 8, 27.5 with 32); few tokens are spread over the SMs
         const int batch = 4 * kThreads / std::max(lanes, 4) / w.heads;
         part.per_block = int(std::max<int64_t>(1, std::min<int64_t>({kMaxWriteTokens, batch, op::div_up(part.tokens, 2 * sms)})));
         part.alone = part.tokens <= kAloneTokens;
