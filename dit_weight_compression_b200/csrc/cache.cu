@@ -619,6 +619,30 @@ int make_views(const ep_cache* caches, const ep_heads* h, int n, const char* who
     return EP_OK;
 }
 
+// Whether two caches (of make_views) have bytes in common: a write's blocks for one would race with the other's.
+bool share_bytes(const ep_cache* c, const CacheView* v) {
+    struct Range { uintptr_t at, end; } r[2][2];
+    for (int i = 0; i < 2; ++i) {
+        const uintptr_t rows = uintptr_t(c[i].n_pages) * uintptr_t(c[i].page_size) * uintptr_t(c[i].heads);
+        const uintptr_t data = reinterpret_cast<uintptr_t>(c[i].data), scales = reinterpret_cast<uintptr_t>(c[i].scales);
+        r[i][0] = {data, data + rows * uintptr_t(v[i].row_bytes)};
+        r[i][1] = {scales, scales + rows * uintptr_t(v[i].scale_bytes)};
+    }
+    for (const Range& x : r[0])
+        for (const Range& y : r[1])
+            if (x.at < y.end && y.at < x.end) return true;
+    return false;
+}
+
+// Whether the rows lie apart: a token's heads within its stride, or a head's tokens within its own.
+bool rows_apart(const ep_heads& h) {
+    const int64_t t = h.tokens - 1, n = h.heads - 1, d = h.head_dim;
+    const auto nested = [d](int64_t few, int64_t inner, int64_t many, int64_t outer) {  // few + 1 rows, inner apart, and so on
+        return (few <= 0 || inner >= d) && (many <= 0 || (outer >= d && (few <= 0 || (outer - d) / few >= inner)));
+    };
+    return nested(n, h.head_stride, t, h.token_stride) || nested(t, h.token_stride, n, h.head_stride);
+}
+
 // The current device, which must be the caches' and heads' own.
 int device_of(const ep_cache* caches, const ep_heads* h, int n, const char* who, int& sms) {
     int dev = 0;
@@ -644,6 +668,7 @@ extern "C" int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n
     if (rc != EP_OK) return rc;
     const int64_t tokens = src[0].tokens;
     if (tokens > 0 && (!slots || !op::aligned(slots, 8))) return set_error(EP_ERR_ARG, "ep_cache_write: slots are NULL or misaligned");
+    if (n == 2 && share_bytes(caches, w.c)) return set_error(EP_ERR_ARG, "ep_cache_write: the two caches share memory");
     rc = device_of(caches, src, n, "ep_cache_write", sms);
     if (rc != EP_OK || tokens == 0 || caches[0].n_pages == 0) return rc;
     const int lanes = lanes_of(w.c, n);
@@ -685,6 +710,10 @@ extern "C" int ep_cache_read(const ep_cache* caches, const ep_heads* out, int n,
         return set_error(EP_ERR_ARG, "ep_cache_read: bad sequence count or page table");
     if (!cu_seqlens || !op::aligned(cu_seqlens, 4) || (n_seqs > 0 && pages_per_seq > 0 && (!page_table || !op::aligned(page_table, 4))))
         return set_error(EP_ERR_ARG, "ep_cache_read: page_table or cu_seqlens is NULL or misaligned");
+    for (int i = 0; i < n; ++i)
+        if (!rows_apart(out[i])) return set_error(EP_ERR_ARG, "ep_cache_read: rows of out overlap");
+    if (n == 2 && out[0].tokens > 0 && out[0].data == out[1].data)
+        return set_error(EP_ERR_ARG, "ep_cache_read: the two outputs are one");
     rc = device_of(caches, out, n, "ep_cache_read", sms);
     if (rc != EP_OK || n_seqs == 0 || out[0].tokens == 0) return rc;
     r.page_table = page_table;

@@ -315,7 +315,7 @@ typedef struct {
 /*
  * Quantise tokens into their slots.
  *   caches  n caches (1 or 2: keys and values) on the current device, of one geometry apart from
- *           head_dim.
+ *           head_dim, without a byte in common.
  *   src     n sources; src[i] matches caches[i] in heads and head_dim, all have the same tokens.
  *   slots   one int64 slot a token, device memory.  A token whose slot is negative or past the last
  *           page is skipped (padding).  When a slot is named more than once, the last token that
@@ -331,8 +331,9 @@ int ep_cache_write(const ep_cache* caches, const ep_heads* src, int n, const int
  * token cu_seqlens[i] + p of out: payload * scale as a float, then rounded to out's type (only EP_INT8
  * needs the first rounding).
  *   caches      n caches (1 or 2) as for ep_cache_write.
- *   out         n outputs with the same tokens; out[i] matches caches[i] in heads and head_dim; rows
- *               may not overlap.
+ *   out         n outputs with the same tokens; out[i] matches caches[i] in heads and head_dim; its
+ *               rows may not overlap (a token's heads lie within token_stride, or a head's tokens
+ *               within head_stride), nor may those of two outputs.
  *   page_table  n_seqs x table_stride int32 in device memory, of which the first `pages_per_seq` of
  *               a row are used.  A position whose page is negative, not below n_pages, or past
  *               pages_per_seq reads as zeros.

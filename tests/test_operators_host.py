@@ -166,3 +166,49 @@ def test_codec_refuses_the_new_containers(ep):
     t = ep.EpTensor(P, -1, 6, 4, 64, 64)
     h = ctypes.c_void_p()
     assert ep.lib().ep_compress(ctypes.byref(t), 4.0, ctypes.byref(h)) == DTYPE
+
+
+# For calls that every check of pointers and sizes lets pass: the device that they name is not there, so
+# they end before a launch with a GPU as well as without one.
+NOWHERE = 4000
+
+
+def refused(ep, rc, words):
+    """Whether a call that ended with an error did so for `words`."""
+    assert rc != 0
+    return words in ep.lib().ep_last_error().decode()
+
+
+def test_cache_write_into_one_pool_refused(ep):
+    """Keys and values of one call may not share bytes (64 slots, 2 heads of 64: 8192 bytes of rows and 512
+    of scales a cache)."""
+    L, h = ep.lib(), heads(ep, device=NOWHERE)
+    k = cache(ep, data=P, scales=P + 8192, device=NOWHERE)
+    for data, scales, want in ((0, 32768, True), (16384, 8192, True), (8176, 32768, True), (8688, 32768, True),
+                               (16384, 8188, True), (16384, 8700, True), (8704, 32768, False), (32768, 8704, False)):
+        v = cache(ep, data=P + data, scales=P + scales, device=NOWHERE)
+        for two in ((k, v), (v, k)):
+            rc = L.ep_cache_write((ep.EpCache * 2)(*two), (ep.EpHeads * 2)(h, h), 2, P, None)
+            assert refused(ep, rc, "share memory") == want, (data, scales)
+            assert not want or rc == ARG
+
+
+def test_cache_read_rows_apart(ep):
+    """Output rows that overlap are refused; either order of tokens and heads is not."""
+    L, r, c = ep.lib(), ctypes.byref, cache(ep, device=NOWHERE)
+    big = 1 << 62
+
+    def overlap(c=c, **kw):
+        rc = L.ep_cache_read(r(c), r(heads(ep, device=NOWHERE, **kw)), 1, P, 4, 4, 2, P, None)
+        return refused(ep, rc, "overlap")
+    for ts, hs, want in ((128, 0, True), (0, 64, True), (127, 64, True), (128, 63, True), (64, 64, True), (64, 319, True),
+                         (big, big, True), (64, big, False), (big, 64, False), (128, 64, False), (64, 320, False),
+                         (65, 400, False)):
+        assert overlap(ts=ts, hs=hs) == want, (ts, hs)
+    assert not overlap(tokens=1, ts=0) and not overlap(tokens=0, ts=0) and overlap(tokens=1, ts=0, hs=63)
+    one = cache(ep, heads=1, device=NOWHERE)
+    assert not overlap(one, n=1, ts=64, hs=0) and overlap(one, n=1, ts=63, hs=0)
+    h = heads(ep, device=NOWHERE)
+    for other, want in ((h, True), (heads(ep, data=P + 4096, device=NOWHERE), False)):
+        rc = L.ep_cache_read((ep.EpCache * 2)(c, c), (ep.EpHeads * 2)(h, other), 2, P, 4, 4, 2, P, None)
+        assert refused(ep, rc, "outputs are one") == want
