@@ -63,6 +63,13 @@ __device__ __forceinline__ float bias_at(const MatmulArgs& a, int64_t n) {
     return __half2float(static_cast<const __half*>(a.bias)[n]);
 }
 
+// The tensor scales, the smaller first: a sum times their product, which need not be a float (two of
+// 2^64 and a sum that is zero), is formed as (sum * x) * y, whose first step stays within fp32 where the whole does.
+__device__ __forceinline__ float2 tensor_scales(const MatmulArgs& a) {
+    const float ga = *a.ga, gb = *a.gb;
+    return fabsf(ga) <= fabsf(gb) ? make_float2(ga, gb) : make_float2(gb, ga);
+}
+
 // The first n of four neighbouring elements of row i from column j (a multiple of 4) on.
 __device__ __forceinline__ void store4(const MatmulArgs& a, int64_t i, int64_t j, int n, const float* v) {
     const int64_t at = i * a.stride + j;
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
     ok &= bar_wait(done, 0);
     fence_after();
 
-    const float alpha = *a.ga * *a.gb;
+    const float2 g = tensor_scales(a);
     float* part = reinterpret_cast<float*>(smem);  // [token][row of b]
     if (warp >= 2) {
         const int row = (warp % 4) * 32 + lane;
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
             v[3] += f.w;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __fmaf_rn(v[j], alpha, bias[j]);
+        for (int j = 0; j < 4; ++j) v[j] = __fmaf_rn(v[j] * g.x, g.y, bias[j]);
         if (ok && n > 0) store4(a, int64_t(m0) + c, col, n, v);
     }
     __syncwarp();
@@ -433,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
             }
         }
     } else {
-        const float alpha = *m.ga * *m.gb;
+        const float2 g = tensor_scales(m);
         const int quarter = warp % 4, half = (warp - 2) / 4;  // 32 lanes x 128 columns a warp
         int n = 0;
         for (int t = pair; t < tiles; t += pairs, ++n) {
@@ -467,11 +474,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
                                  : "r"(buf + 4 * c));
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        r[c / 16][c % 16 + j] = __float_as_uint(__fmaf_rn(__uint_as_float(r[c / 16][c % 16 + j]), alpha, v[j]));
+                        r[c / 16][c % 16 + j] = __float_as_uint(__fmaf_rn(__uint_as_float(r[c / 16][c % 16 + j]) * g.x, g.y, v[j]));
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < 128; ++c) r[c / 16][c % 16] = __float_as_uint(__uint_as_float(r[c / 16][c % 16]) * alpha);
+                for (int c = 0; c < 128; ++c) r[c / 16][c % 16] = __float_as_uint(__uint_as_float(r[c / 16][c % 16]) * g.x * g.y);
             }
             if (m.out_dtype == EP_F32) {
 #pragma unroll

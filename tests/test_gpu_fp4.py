@@ -275,6 +275,24 @@ def test_matmul_general_scales_and_bias(ep, fmt, dtype, m, n, k):
     ep.op_status()
 
 
+@pytest.mark.parametrize("ga,gb", [(100, 90), (-100, -45), (-60, -100), (110, -110), (-90, 117), (127, 127)])
+@pytest.mark.parametrize("m", [2, 140, 2400])
+def test_matmul_tensor_scales_far_apart(ep, m, ga, gb):
+    """2^ga and 2^gb whose product is no float: the sums here are multiples of 2^-4 below 2^14, so the
+    result is the exact one rounded once, and sums that are zero stay zero."""
+    a, av = random_fp4(ep, m, 64, "nvfp4", 20, True)
+    b, bv = random_fp4(ep, 2300, 64, "nvfp4", 21, True)
+    a.data[0] = 0
+    av[0] = 0
+    for sign in (1.0, -1.0):
+        a.tensor_scale.fill_(sign * 2.0 ** ga)
+        b.tensor_scale.fill_(2.0 ** gb)
+        want = ((av @ bv.T) * (sign * 2.0 ** ga) * 2.0 ** gb).float()
+        assert torch.equal(ep.fp4_matmul(a, b, dtype=torch.float32), want)
+        bias = torch.zeros(2300, device="cuda")
+        assert torch.equal(ep.fp4_matmul(a, b, bias=bias, dtype=torch.float32), want)
+
+
 @pytest.mark.parametrize("m", [3, 150, 2400])
 def test_matmul_strided_and_misaligned_out(ep, m):
     """Windows of a wider output: the neighbours stay as they were."""
