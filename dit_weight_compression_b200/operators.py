@@ -158,10 +158,11 @@ class FP4Tensor:
                 if cols % 2:
                     t.data[:, cols // 2] &= 15
             i, j = t._scale_tiles
-            s = torch.zeros(i * 128, j * 4, dtype=torch.uint8, device=dev)
-            s[:rows, :blocks] = scale_rows if format == "mxfp4" else scale_rows & 0x7F  # E4M3 scales have no sign
-            # four scales of a row at a time: tiles of 32 x 4 words
-            t.scales.view(torch.int32).view(i, j, 32, 4).copy_(s.view(torch.int32).view(i, 4, 32, j).permute(0, 3, 2, 1))
+            if i and j:  # a matrix without rows or columns has no scales
+                s = torch.zeros(i * 128, j * 4, dtype=torch.uint8, device=dev)
+                s[:rows, :blocks] = scale_rows if format == "mxfp4" else scale_rows & 0x7F  # E4M3 scales have no sign
+                # four scales of a row at a time: tiles of 32 x 4 words
+                t.scales.view(torch.int32).view(i, j, 32, 4).copy_(s.view(torch.int32).view(i, 4, 32, j).permute(0, 3, 2, 1))
             t.tensor_scale.copy_(tensor_scale.reshape(1))
         return t
 

@@ -49,3 +49,20 @@ def test_matmul_tensor_scale_not_finite_or_zero(ep, m):
             b.tensor_scale.fill_(gb)
             want = ((av @ bv.T) * (ga * gb)).float()
             assert torch.equal(ep.fp4_matmul(a, b, dtype=torch.float32).nan_to_num(nan=7e30), want.nan_to_num(nan=7e30))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("shape", [(5, 0), (0, 64), (0, 0), (200, 0)])
+def test_from_rows_empty(ep, fmt, shape):
+    """Rows made elsewhere of a matrix without rows or columns, as the quantiser makes it."""
+    rows, cols = shape
+    data = torch.zeros(rows, 16 * -(-cols // 32), dtype=torch.uint8, device="cuda")
+    sc = torch.zeros(rows, -(-cols // R.BLOCK[fmt]), dtype=torch.uint8, device="cuda")
+    q = ep.FP4Tensor.from_rows(data, sc, torch.ones(1, device="cuda"), shape, fmt)
+    like = ep.fp4_quantize(torch.zeros(shape, device="cuda"), fmt)
+    assert q.shape == like.shape and q.nbytes == like.nbytes and q.scales.shape == like.scales.shape
+    assert q.scale_rows().shape == sc.shape and float(q.tensor_scale) == 1.0
+    assert ep.fp4_dequantize(q).shape == shape
+    x = ep.fp4_quantize(torch.ones(3, cols, device="cuda"), fmt)
+    y = ep.fp4_matmul(x, q, dtype=torch.float32)
+    assert y.shape == (3, rows) and not y.any()
