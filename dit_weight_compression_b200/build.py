@@ -24,7 +24,7 @@ PLAIN = ["api.cpp", "encoder.cpp", "decode.cu", "encode_gpu.cu", "ops.cpp", "fp4
 UNIT_OUTS = range(7)
 UNIT_LAYS = (10, 11, 12, 13, 14, 15)
 HEADERS = ["format.h", "blob.h", "tables.h", "decode_launch.h", "decode_device.cuh", "ops.h", "microscale.cuh",
-           "tcgen05.cuh"]
+           "tcgen05.cuh", "fp4_shape.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

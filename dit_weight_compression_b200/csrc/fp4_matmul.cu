@@ -5,6 +5,7 @@
 #include <string>
 
 #include "blob.h"
+#include "fp4_shape.h"
 #include "microscale.cuh"
 #include "ops.h"
 #include "tcgen05.cuh"
@@ -552,12 +553,11 @@ bool operand_map(CUtensorMap* map, const ep_fp4_tensor* t, int box_rows) {
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Clusters of `split` CTAs of a variant that fit the device at one time (looked up once), after setting
-// its kernel's shared memory.
-constexpr int kMaxSplit = 8;
+// Clusters of `split` CTAs of a variant that fit the device at one time (looked up once; 0: none does), after
+// setting its kernel's shared memory.
 template <int NT, bool NV>
 cudaError_t clusters_of(int dev, int split, int& clusters) {
-    static std::atomic<int> known[kMaxDevices][kMaxSplit + 1];
+    static std::atomic<int> known[kMaxDevices][fp4::kMaxSplit + 1];
     clusters = known[dev][split].load(std::memory_order_relaxed);
     if (clusters > 0) return cudaSuccess;
     const auto kernel = fp4_split_kernel<NT, NV>;
@@ -575,7 +575,6 @@ cudaError_t clusters_of(int dev, int split, int& clusters) {
         cfg.numAttrs = 1;
         e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
     }
-    if (e == cudaSuccess && clusters < 1) e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess) known[dev][split].store(clusters, std::memory_order_relaxed);
     return e;
 }
@@ -590,7 +589,7 @@ bool scale_map(CUtensorMap* map, const ep_fp4_tensor* t, int scale_tiles, int bo
               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Pairs of CTAs that fit the device at one time (looked up once), after setting the kernel's shared memory.
+// Pairs of CTAs that fit the device at one time (looked up once; 0: none does), after setting the kernel's shared memory.
 template <bool NV>
 cudaError_t pairs_of(int dev, int& pairs) {
     static std::atomic<int> known[kMaxDevices];
@@ -605,13 +604,12 @@ cudaError_t pairs_of(int dev, int& pairs) {
         cfg.dynamicSmemBytes = PairGeo<NV>::kSmem;
         e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
     }
-    if (e == cudaSuccess && pairs < 1) e = cudaErrorInvalidConfiguration;
     if (e == cudaSuccess) known[dev].store(pairs, std::memory_order_relaxed);
     return e;
 }
 
 template <bool NV>
-int run_pairs(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int dev, cudaStream_t st) {
+int run_pairs(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& args, int pairs, cudaStream_t st) {
     CUtensorMap a_map, b_map, as_map, bs_map;
     if (!operand_map(&a_map, a, 128) || !operand_map(&b_map, b, 128) ||
         !scale_map(&as_map, a, args.scale_tiles, PairGeo<NV>::kScaleTiles) ||
@@ -624,30 +622,16 @@ int run_pairs(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& 
     // `group` of them (8192 x 28672 x 8192: 745 us with 4, 710 with 8, 691 with 16, 694 with 32)
     p.group = int(std::max<int64_t>(4, std::min<int64_t>(16, (int64_t(32) << 20) / (256 * op::fp4_row_bytes(a->cols)))));
     if (int64_t(p.a_tiles) * p.b_tiles > 0x7fffffff) return set_error(EP_ERR_SHAPE, "ep_fp4_matmul: too many tiles");
-    int pairs = 0;
-    cudaError_t e = pairs_of<NV>(dev, pairs);
-    if (e == cudaSuccess) {
-        pairs = std::min(pairs, p.a_tiles * p.b_tiles);
-        e = op::launch(fp4_pair_kernel<NV>, dim3(unsigned(2 * pairs)), dim3(PairGeo<NV>::kThreads), PairGeo<NV>::kSmem, st, a_map, b_map,
-                       as_map, bs_map, p);
-    }
+    const cudaError_t e = op::launch(fp4_pair_kernel<NV>, dim3(unsigned(2 * std::min(pairs, p.a_tiles * p.b_tiles))),
+                                     dim3(PairGeo<NV>::kThreads), PairGeo<NV>::kSmem, st, a_map, b_map, as_map, bs_map, p);
     if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_matmul: ") + cudaGetErrorString(e));
     return EP_OK;
 }
 
-// CTAs of one tile: the most whose clusters all fit the device at once, with four stages each.  (4096
-// outputs of 4096 for one token: 5.4 us with 4, 6.5 with 8 of two stages; 300 tokens: 11.1 us with 2, 16.7
-// with 3, which need a second round.)
 template <int NT, bool NV>
 cudaError_t split_of(int dev, int64_t tiles, int steps, int& split) {
-    int clusters = 0;
-    split = std::min(kMaxSplit, (steps + 3) / 4);
-    cudaError_t e = clusters_of<NT, NV>(dev, 1, clusters);
-    for (; e == cudaSuccess && split > 1; --split) {
-        e = clusters_of<NT, NV>(dev, split, clusters);
-        if (tiles <= clusters) break;
-    }
-    return e;
+    return fp4::split_of(tiles, steps, [dev](int n, int& clusters) { return clusters_of<NT, NV>(dev, n, clusters); },
+                         cudaErrorInvalidConfiguration, split);
 }
 
 template <int NT, bool NV>
@@ -677,13 +661,15 @@ int matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& arg
     // worth sharing among three CTAs or more (200 tokens, 2048 outputs of 8192: 7.7 us so, 14.1 in pairs;
     // 256, 4096 of 4096: 8.9 and 9.8; 384, which can share by two only: 10.5 and 10.0; 130, 28672 of 1024:
     // 13.9 and 10.1).
-    int split = kMaxSplit;
+    // Without room for a pair of CTAs (a part of a GPU) every product is a short one.
+    int split = fp4::kMaxSplit, pairs = 0;
     if (m > 128) {
-        const cudaError_t e = split_of<128, NV>(dev, int64_t(args.n_tiles) * op::div_up(m, 128), args.steps, split);
+        cudaError_t e = split_of<128, NV>(dev, int64_t(args.n_tiles) * op::div_up(m, 128), args.steps, split);
+        if (e == cudaSuccess && split < 3) e = pairs_of<NV>(dev, pairs);
         if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_fp4_matmul: ") + cudaGetErrorString(e));
     }
-    if (split >= 3) return run_split<128, NV>(a, b, args, dev, st);
-    return run_pairs<NV>(a, b, args, dev, st);
+    if (pairs == 0) return run_split<128, NV>(a, b, args, dev, st);
+    return run_pairs<NV>(a, b, args, pairs, st);
 }
 
 }  // namespace
