@@ -525,6 +525,15 @@ __global__ void __launch_bounds__(256) bias_kernel(const MatmulArgs a, int64_t r
     }
 }
 
+// A wait that can only give up: a barrier that nothing arrives on.
+__global__ void __launch_bounds__(32) wait_probe_kernel(uint32_t tries) {
+    __shared__ __align__(8) uint64_t bar;
+    ms::wait_for_stream();
+    if (threadIdx.x == 0) bar_init(smem_addr(&bar), 1);
+    __syncthreads();
+    if (!bar_wait(smem_addr(&bar), 0, tries)) atomicOr(&ep_op_status_word, 1u);
+}
+
 // ---- host side -------------------------------------------------------------------------------------
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -723,6 +732,14 @@ extern "C" int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, con
         return EP_OK;
     }
     return a->format == EP_NVFP4 ? matmul<true>(a, b, args, dev, st) : matmul<false>(a, b, args, dev, st);
+}
+
+extern "C" int ep_op_wait_probe(uint32_t wait_tries, void* stream) {
+    clear_error();
+    if (wait_tries == 0) return set_error(EP_ERR_ARG, "ep_op_wait_probe: zero limit");
+    const cudaError_t e = op::launch(wait_probe_kernel, dim3(1), dim3(32), 0, static_cast<cudaStream_t>(stream), wait_tries);
+    if (e != cudaSuccess) return set_error(EP_ERR_CUDA, std::string("ep_op_wait_probe: ") + cudaGetErrorString(e));
+    return EP_OK;
 }
 
 extern "C" int ep_op_status(void* stream) {

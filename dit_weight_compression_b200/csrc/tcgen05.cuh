@@ -42,8 +42,8 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 // Bounded wait for the phase of the given parity; false when it gave up.
 constexpr uint32_t kWaitTries = 1u << 22;
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kWaitTries; ++i)
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t tries = kWaitTries) {
+    for (uint32_t i = 0; i < tries; ++i)
         if (bar_try(bar, parity)) return true;
     return false;
 }

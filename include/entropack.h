@@ -351,6 +351,12 @@ int ep_cache_read(const ep_cache* caches, const ep_heads* out, int n, const int3
  * for the tensor cores (its output is then incomplete). */
 int ep_op_status(void* stream);
 
+/* Test hook for the bounded waits of ep_fp4_matmul: a kernel that polls, `wait_tries` times at most, a
+ * shared-memory barrier that nothing arrives on.  It gives up, sets the status word as a product would,
+ * and ends; nothing is read or written, and the context stays usable.  Returns EP_ERR_ARG (zero limit),
+ * EP_ERR_CUDA. */
+int ep_op_wait_probe(uint32_t wait_tries, void* stream);
+
 /* Stored bits per element: 8 * (stored bytes including metadata) / (rows * cols)
  * ("EntroPack lattice compression", section "Encoding and reconstruction": the reported rate
  * counts every stored byte, metadata included, as bits per element).  Returns -1.0 for a NULL

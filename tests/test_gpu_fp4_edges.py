@@ -66,3 +66,22 @@ def test_from_rows_empty(ep, fmt, shape):
     x = ep.fp4_quantize(torch.ones(3, cols, device="cuda"), fmt)
     y = ep.fp4_matmul(x, q, dtype=torch.float32)
     assert y.shape == (3, rows) and not y.any()
+
+
+def test_wait_that_gives_up_is_reported_once(ep):
+    """A kernel whose barrier no copy ever reaches gives up after its short limit: the status is raised once,
+    and the next product is right."""
+    a, av = random_fp4(ep, 30, 256, "nvfp4", 1, True)
+    b, bv = random_fp4(ep, 300, 256, "nvfp4", 2, True)
+    L, st = ep.lib(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    ep.op_status()
+    assert L.ep_op_wait_probe(0, st) == -1
+    ep.op_status()
+    for _ in range(2):
+        assert L.ep_op_wait_probe(2000, st) == 0, L.ep_last_error()
+        with pytest.raises(ep.EPError) as e:
+            ep.op_status()
+        assert e.value.code == -6 and "gave up" in str(e.value)
+        ep.op_status()
+        assert torch.equal(ep.fp4_matmul(a, b, dtype=torch.float32).double(), av @ bv.T)
+        ep.op_status()
