@@ -92,6 +92,8 @@ SIGNATURES = {
     "ep_cache_read": (_I, [ctypes.POINTER(EpCache), ctypes.POINTER(EpHeads), _I, _P, _I64, _I64, _I, _P, _P]),
     "ep_op_status": (_I, [_P]),
     "ep_op_wait_probe": (_I, [ctypes.c_uint32, _P]),
+    "ep_fp4_matmul_probe": (_I, [ctypes.POINTER(EpFP4Tensor), ctypes.POINTER(EpFP4Tensor), ctypes.POINTER(EpTensor), _I,
+                                 ctypes.c_uint32, _P]),
     "ep_blob_free": (None, [_P]),
     "ep_last_error": (ctypes.c_char_p, []),
 }

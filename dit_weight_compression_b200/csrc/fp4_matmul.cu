@@ -36,6 +36,8 @@ struct MatmulArgs {
     int n_tiles;               // tiles of 128 rows of b
     int out_dtype;
     int width;                 // alignment of out's rows: 16, 8 or 4 bytes, or 1 for their elements'
+    int gives_up;              // 0, or one more than the tile that acts as if a wait for its copies had run out
+    uint32_t tries;            // limit of the waits of one role for another
 };
 
 // Tile sizes, stage layout and tensor memory columns of a variant with tiles of NT tokens.
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
     const uint32_t bars = base + G::kStages * G::kStage;  // full, empty of each stage; done; the TMEM address
     auto full = [&](int s) { return bars + 8 * s; };
     auto empty = [&](int s) { return bars + 8 * (G::kStages + s); };
-    const uint32_t done = bars + 16 * G::kStages, slot = done + 8;
+    const uint32_t done = bars + 16 * G::kStages, slot = done + 8, lost = slot + 4;
     const int warp = int(uniform(threadIdx.x / 32)), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank(), ranks = cluster_ranks();
     const int tile = int(blockIdx.x / ranks);
@@ -135,6 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
             bar_init(empty(s), 1);
         }
         bar_init(done, 1);
+        store_u32(lost, 0);
         prefetch_map(&b_map);
         prefetch_map(&a_map);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -208,11 +211,13 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
             }
         }
         if (leader) commit(done);
+        if (a.gives_up == tile + 1 && rank == ranks - 1) ok = false;
     }
     __syncwarp();
     // every warp: the sums are ready, and no copy or product uses the stages any more
     ok &= bar_wait(done, 0);
     fence_after();
+    if (!ok) store_u32(lost, 1);  // some of these sums are not whole
 
     const float ga = *a.ga, gb = *a.gb;
     float* part = reinterpret_cast<float*>(smem);  // [token][row of b]
@@ -230,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
     __syncwarp();
     if (ranks > 1) cluster_sync();
     else __syncthreads();
+    const uint32_t missing = uint32_t(lane) < ranks ? peer_load_u32(lost, uint32_t(lane)) : 0;  // of each CTA
     const float2 g = tensor_scales(ga, gb);
     const int c0 = NT * int(rank) / int(ranks), c1 = NT * (int(rank) + 1) / int(ranks);
     const int64_t col = int64_t(n0) + 4 * lane;
@@ -248,7 +254,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = __fmaf_rn(v[j] * g.x, g.y, bias[j]);
-        if (ok && n > 0) store4(a, int64_t(m0) + c, col, n, v);
+        // a tile with a part missing is not written (asked here, where the loads of the sums have covered the answer's way)
+        if (!__any_sync(ms::kFullMask, missing) && n > 0) store4(a, int64_t(m0) + c, col, n, v);
     }
     __syncwarp();
     if (ranks > 1) cluster_sync();  // no CTA leaves while another reads its sums
@@ -354,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
     const uint32_t out_bufs = base + G::kStages * G::kStage, bars = out_bufs + 8 * G::kOut;
     auto full = [&](int s) { return bars + 8 * s; };  // used in the first CTA
     auto empty = [&](int s) { return bars + 8 * (G::kStages + s); };
-    const uint32_t summed = bars + 16 * G::kStages, taken = summed + 8, slot = taken + 8;
+    const uint32_t summed = bars + 16 * G::kStages, taken = summed + 8, drained = taken + 8, slot = drained + 8;
     const int warp = int(uniform(threadIdx.x / 32)), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, tiles = args.a_tiles * args.b_tiles;
@@ -366,6 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
         }
         bar_init(summed, 1);
         bar_init(taken, 16);  // the 8 reading warps of both CTAs
+        bar_init(drained, 1);
         prefetch_map(&a_map);
         prefetch_map(&b_map);
         prefetch_map(&as_map);
@@ -394,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
             const int a_scales = (2 * ta + int(rank)) * m.scale_tiles, b_scales = 2 * tb * m.scale_tiles;
             for (int k = 0; k < m.steps; ++k, ++it) {
                 const int s = it % G::kStages;
-                if (it >= G::kStages && !(ok = bar_wait(empty(s), (it / G::kStages - 1) & 1))) break;
+                if (it >= G::kStages && !(ok = bar_wait(empty(s), (it / G::kStages - 1) & 1, m.tries))) break;
                 const uint32_t st = base + s * G::kStage;
                 if (leader) {
                     if (rank == 0) bar_expect(full(s), 2 * G::kStage);
@@ -417,11 +425,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
             const bool leader = elect_one();
             int it = 0, n = 0;
             for (int t = pair; t < tiles && ok; t += pairs, ++n) {
-                if (n > 0 && !(ok = bar_wait(taken, (n - 1) & 1))) break;
+                if (n > 0 && !(ok = bar_wait(taken, (n - 1) & 1, m.tries))) break;
                 fence_after();
                 for (int k = 0; k < m.steps; ++k, ++it) {
                     const int s = it % G::kStages;
-                    if (!(ok = bar_wait(full(s), (it / G::kStages) & 1))) break;
+                    if (!(ok = bar_wait(full(s), (it / G::kStages) & 1, m.tries))) break;
                     fence_after();
                     const uint32_t st = base + s * G::kStage;
                     const uint32_t sa = tmem + 256 + s * G::kScaleCols, sb = sa + 4 * G::kScaleTiles;
@@ -444,7 +452,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
                         commit_pair(empty(s));
                     }
                 }
+                if (m.gives_up == t + 1) ok = false;
+                if (!ok) break;  // sums of which a part is missing are not handed on: the readers give up as well
                 if (leader) commit_pair(summed);
+            }
+            if (!ok) {  // the products on their way end before anything is taken down
+                if (leader) commit_pair(drained);
+                __syncwarp();
+                bar_wait(drained, 0);
             }
         }
     } else {
@@ -454,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGeo<NV>::kThread
         for (int t = pair; t < tiles; t += pairs, ++n) {
             int ta, tb;
             pair_tile(args, t, ta, tb);
-            if (!(ok = bar_wait(summed, n & 1))) break;
+            if (!(ok = bar_wait(summed, n & 1, m.tries))) break;
             fence_after();
             uint32_t r[8][16];
 #pragma unroll
@@ -686,7 +701,9 @@ int matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const MatmulArgs& arg
 
 using namespace ep;
 
-extern "C" int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const void* bias, const ep_tensor* out, void* stream) {
+namespace {
+
+int product(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const void* bias, const ep_tensor* out, int gives_up, uint32_t tries, void* stream) {
     clear_error();
     if (!a || !b || !out) return set_error(EP_ERR_ARG, "ep_fp4_matmul: NULL argument");
     int rc = op::check_fp4(a, "ep_fp4_matmul");
@@ -708,6 +725,8 @@ extern "C" int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, con
         return set_error(EP_ERR_ARG, "ep_fp4_matmul: a tensor is not on the current device");
     if (empty) return EP_OK;
     MatmulArgs args = {};
+    args.gives_up = gives_up;
+    args.tries = tries;
     args.ga = a->tensor_scale;
     args.gb = b->tensor_scale;
     args.bias = bias;
@@ -732,6 +751,21 @@ extern "C" int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, con
         return EP_OK;
     }
     return a->format == EP_NVFP4 ? matmul<true>(a, b, args, dev, st) : matmul<false>(a, b, args, dev, st);
+}
+
+}  // namespace
+
+extern "C" int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const void* bias, const ep_tensor* out, void* stream) {
+    return product(a, b, bias, out, 0, kWaitTries, stream);
+}
+
+extern "C" int ep_fp4_matmul_probe(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const ep_tensor* out, int tile, uint32_t wait_tries,
+                                   void* stream) {
+    if (tile < 0 || tile == 0x7fffffff || wait_tries == 0) {
+        clear_error();
+        return set_error(EP_ERR_ARG, "ep_fp4_matmul_probe: bad tile or zero limit");
+    }
+    return product(a, b, nullptr, out, tile + 1, wait_tries, stream);
 }
 
 extern "C" int ep_op_wait_probe(uint32_t wait_tries, void* stream) {

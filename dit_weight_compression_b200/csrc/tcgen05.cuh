@@ -195,6 +195,7 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void store_u32(uint32_t smem, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(smem), "r"(v) : "memory"); }
 // A word / float4 of the shared memory of CTA `rank` of the cluster, at this CTA's own address.
 __device__ __forceinline__ uint32_t peer_load_u32(uint32_t smem, uint32_t rank) {
     uint32_t a, v;

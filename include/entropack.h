@@ -272,7 +272,7 @@ int ep_decompress_fp4(const ep_blob* b, const ep_fp4_tensor* out, double tensor_
  * Sums are held in fp32, scaled, biased and then rounded once.  The order of a sum depends on the
  * sizes only, so the same operands give the same bits.  With no columns the result is the bias (or
  * 0).  out may not overlap the operands.  Errors as for ep_fp4_quantize; a kernel that gave up
- * waiting for its copies reports it through ep_op_status().
+ * waiting for its copies reports it through ep_op_status() and leaves the tiles concerned unwritten.
  */
 int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const void* bias, const ep_tensor* out, void* stream);
 
@@ -356,6 +356,14 @@ int ep_op_status(void* stream);
  * and ends; nothing is read or written, and the context stays usable.  Returns EP_ERR_ARG (zero limit),
  * EP_ERR_CUDA. */
 int ep_op_wait_probe(uint32_t wait_tries, void* stream);
+
+/* The same for a product that gives up in the middle: ep_fp4_matmul without a bias, in which tile `tile` acts
+ * as if one of the waits for its copies had run out (every copy is waited for all the same).  That tile is
+ * not written, nor are those that the same CTAs would have computed after it, and the status word is set.
+ * `wait_tries` limits the waits of one part of the kernel for another (about 4 us each).  Returns EP_ERR_ARG
+ * (negative tile, zero limit) and the errors of ep_fp4_matmul. */
+int ep_fp4_matmul_probe(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const ep_tensor* out, int tile, uint32_t wait_tries,
+                        void* stream);
 
 /* Stored bits per element: 8 * (stored bytes including metadata) / (rows * cols)
  * ("EntroPack lattice compression", section "Encoding and reconstruction": the reported rate

@@ -85,3 +85,29 @@ def test_wait_that_gives_up_is_reported_once(ep):
         ep.op_status()
         assert torch.equal(ep.fp4_matmul(a, b, dtype=torch.float32).double(), av @ bv.T)
         ep.op_status()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m,n,k,tile,rows,cols", [
+    (100, 600, 4096, 3, (0, 100), (384, 512)),     # CTAs that share a tile: the last of them gives up
+    (20, 600, 200, 4, (0, 20), (512, 600)),        # a CTA by itself
+    (600, 1030, 512, 7, (256, 512), (512, 768))])  # pairs, a tile each
+def test_tile_given_up_is_not_written(ep, fmt, m, n, k, tile, rows, cols):
+    """A tile that one CTA gave up stays as it was, the others are right, and the status is raised once."""
+    a, av = random_fp4(ep, m, k, fmt, 3, True)
+    b, bv = random_fp4(ep, n, k, fmt, 4, True)
+    want = (av @ bv.T).float()
+    out = torch.full((m, n), 9.5, device="cuda")
+    view = ep.EpTensor(out.data_ptr(), out.device.index, ep.F32, m, n, n)
+    L, st = ep.lib(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert L.ep_fp4_matmul_probe(a._ref, b._ref, ctypes.byref(view), -1, 1, st) == -1
+    assert L.ep_fp4_matmul_probe(a._ref, b._ref, ctypes.byref(view), 0, 0, st) == -1
+    ep.op_status()
+    assert L.ep_fp4_matmul_probe(a._ref, b._ref, ctypes.byref(view), tile, 250000, st) == 0, L.ep_last_error()
+    with pytest.raises(ep.EPError):
+        ep.op_status()
+    want_now = want.clone()
+    want_now[rows[0]:rows[1], cols[0]:cols[1]] = 9.5
+    assert torch.equal(out, want_now)
+    assert torch.equal(ep.fp4_matmul(a, b, dtype=torch.float32), want)
+    ep.op_status()
