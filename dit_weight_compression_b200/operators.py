@@ -2,7 +2,10 @@
 
 Like the codec's binding, this only marshals arguments for ``libentropack.so``; formats, layouts
 and roundings are defined in ``include/entropack.h``.  All tensors are CUDA tensors of one device,
-and every call is asynchronous on the current stream of that device (or on ``stream``).  For example::
+and every call is asynchronous on the current stream of that device (or on ``stream``).  A ``stream`` is
+a torch stream, which holds on to the call's tensors until it is done with them, or a cudaStream_t (a number,
+or in an ExternalStream): then it is the caller who keeps the call's tensors until the work is done.  For
+example::
 
     w4 = ep.fp4_quantize(w, "nvfp4")              # or ep.decompress_fp4(blob, "nvfp4")
     y = ep.fp4_matmul(ep.fp4_quantize(x, "nvfp4"), w4, bias=bias)      # x @ w.T + bias
@@ -55,15 +58,18 @@ _current_device = torch.cuda.current_device
 
 def _on(device: torch.device, stream, *used):
     """(context in which `device` is current and temporaries belong to the call's stream, its handle).
-    `used`: the tensors of the call, whose memory a stream given by hand then holds on to."""
+    `used`: the tensors of the call, whose memory a torch stream given by hand then holds on to.  One
+    that is not torch's own holds on to nothing: the allocator would use its handle when a tensor is freed,
+    which may be long after the caller has destroyed it."""
     index = device.index
     if stream is None:
         return (_HERE if index == _current_device() else torch.cuda.device(device)), _raw_stream(index)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
-    for t in used:
-        if t is not None and t.is_cuda:
-            t.record_stream(stream)
+    if not isinstance(stream, torch.cuda.ExternalStream):
+        for t in used:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
     return torch.cuda.stream(stream), stream.cuda_stream
 
 

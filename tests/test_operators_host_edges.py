@@ -1,4 +1,5 @@
-"""Host checks of the 4-bit and cache operators that need no device: the rule by which CTAs share a tile."""
+"""Host checks of the 4-bit and cache operators that need no device: the rule by which CTAs share a tile, and what
+a stream given by hand holds on to."""
 import os
 import shutil
 import subprocess
@@ -54,3 +55,41 @@ WHOLE = (296, 148, 98, 74, 58, 48, 41, 36)  # a GPU of 148 SMs, two CTAs each
     (1, 32, (0,) * 8, (9, 1)), (1, 32, WHOLE[:7] + (-1,), (7, 8)), (1, 1, (-1,) + WHOLE[1:], (7, 1))])
 def test_ctas_of_a_tile(split_of, tiles, steps, room, want):
     assert split_of(tiles, steps, room) == want
+
+
+class FakeTensor:
+    is_cuda = True
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, s):
+        self.streams.append(s)
+
+
+class FakeStream:
+    """Stands for a torch stream, or with `device` for one made around a handle."""
+
+    def __init__(self, handle, device=None):
+        self.cuda_stream = handle
+
+
+def test_stream_handle_is_not_kept(monkeypatch):
+    """A torch stream holds on to a call's tensors; one given as its handle is never handed to the allocator, which
+    would use it when they are freed, and the default stream's, 0, is torch's own."""
+    import contextlib
+
+    import torch
+
+    from dit_weight_compression_b200 import operators
+    default = FakeStream(0)
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", type("Outside", (FakeStream,), {}))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda d: default)
+    dev, x, s = torch.device("cuda", 0), FakeTensor(), FakeStream(77)
+    assert operators._on(dev, s, x, None)[1] == 77 and x.streams == [s]
+    x.streams.clear()
+    for given in (78, torch.cuda.ExternalStream(78)):
+        assert operators._on(dev, given, x, None)[1] == 78 and x.streams == []
+    assert operators._on(dev, 0, x, None)[1] == 0 and x.streams == [default]
