@@ -316,7 +316,9 @@ __global__ void __launch_bounds__(kThreads) cache_write_any_kernel(const __grid_
 }
 
 // After a write that did not look: each block puts the slots of 512 tokens into a hash table, looks up all
-// slots of the launch, and writes those of its tokens again that come last of several to a slot.
+// slots of the launch, and writes those of its tokens again that come last of several to a slot.  A slot has one
+// entry, the last of the block's tokens that name it, however many do: with an entry for each, 65536 tokens of
+// which half name one slot (padding in a slot of its own) took 3 ms, walking chains of equal entries.
 __device__ __forceinline__ uint32_t slot_hash(int64_t s) {
     return ((uint32_t(s) ^ uint32_t(uint64_t(s) >> 32)) * 2654435761u) >> (32 - kTableBits);
 }
@@ -341,7 +343,14 @@ __global__ void __launch_bounds__(kMendThreads) mend_kernel(const __grid_constan
     if (threadIdx.x == 0) any = 0;
     __syncthreads();
     if (own >= 0)
-        for (uint32_t h = slot_hash(own); atomicCAS(&table[h], -1, int(threadIdx.x)) != -1;) h = (h + 1) % kTable;
+        for (uint32_t h = slot_hash(own);; h = (h + 1) % kTable) {
+            const int i = atomicCAS(&table[h], -1, int(threadIdx.x));
+            if (i == -1) break;
+            if (slot[i] == own) {  // an entry keeps its slot, whichever token it names
+                atomicMax(&table[h], int(threadIdx.x));
+                break;
+            }
+        }
     __syncthreads();
     for (int64_t j0 = threadIdx.x; j0 < a.tokens; j0 += 8 * kMendThreads) {
         int64_t s[8];
@@ -352,8 +361,8 @@ __global__ void __launch_bounds__(kMendThreads) mend_kernel(const __grid_constan
             if (s[u] < 0) continue;
             const int64_t j = j0 + u * kMendThreads - t0;
             int i;
-            for (uint32_t h = slot_hash(s[u]); (i = table[h]) != -1; h = (h + 1) % kTable)
-                if (slot[i] == s[u] && j != i) (j < i ? earlier : later)[i] = any = 1;
+            for (uint32_t h = slot_hash(s[u]); (i = table[h]) != -1 && slot[i] != s[u]; h = (h + 1) % kTable) {}
+            if (i != -1 && j != i) (j < i ? earlier : later)[i] = any = 1;
         }
     }
     __syncthreads();
