@@ -68,6 +68,57 @@ def test_from_rows_empty(ep, fmt, shape):
     assert y.shape == (3, rows) and not y.any()
 
 
+BORDERS = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]
+
+
+def neighbours(v, dtype):
+    """v, and the next numbers of its type on either side, as float64 (v > 0 is one itself)."""
+    t = torch.from_numpy(v).to(dtype)
+    assert torch.equal(t.double(), torch.from_numpy(v))
+    bits = t.view(torch.int32 if dtype == torch.float32 else torch.int16)
+    return [w.view(dtype).double().numpy() for w in (bits, bits - 1, bits + 1)]
+
+
+def border_rows(fmt, dtype):
+    """A row for each block scale q: 6 q first in every block, so that the scale is q, then every border of two
+    codes times q, and its neighbours, with both signs."""
+    sig, exp = (np.arange(8, 16) / 8.0, np.arange(-4, 6)) if fmt == "nvfp4" else (np.ones(1), np.arange(-6, 7))
+    q = (sig[:, None] * np.exp2(exp)[None, :]).reshape(-1)
+    on = q[:, None] * np.array(BORDERS)[None, :]
+    v = np.concatenate(neighbours(on, dtype), 1)
+    v = np.concatenate((v, -v), 1)
+    per = R.BLOCK[fmt] - 1
+    blocks = [np.concatenate((6 * q[:, None], v[:, i:i + per]), 1) for i in range(0, v.shape[1], per)]
+    return q, np.concatenate(blocks, 1)
+
+
+def check_borders_met(x, byte, fmt, dtype, g):
+    """From the stored scales: every significand of a scale meets every border from both sides and on it."""
+    q = R.scale_values(byte, fmt) * g
+    blk = R.BLOCK[fmt]
+    x = np.pad(x, ((0, 0), (0, -x.shape[1] % blk))).reshape(x.shape[0], -1, blk)
+    seen = {(k, b): set() for k in range(3) for b in BORDERS}
+    for b in BORDERS:
+        for k, at in enumerate(neighbours(q * b, dtype)):
+            for sign in (1, -1):
+                hit = (x == sign * at[..., None]).any(-1)
+                seen[(k, b)] |= {(float(s), sign) for s in np.frexp(q[hit])[0]}
+    want = {(s / 16, sign) for s in (range(8, 16) if fmt == "nvfp4" else (8,)) for sign in (1, -1)}
+    assert all(v == want for v in seen.values()), {k: len(v) for k, v in seen.items()}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt,g", [("mxfp4", None), ("nvfp4", None), ("nvfp4", 1.0), ("nvfp4", 2.0)])
+def test_quantize_on_and_beside_every_border(ep, fmt, dtype, g):
+    q, x = border_rows(fmt, dtype)
+    if fmt == "nvfp4" and g is None:  # the largest value is 6 * 60: the scale taken from the data is 2^-2
+        assert R.tensor_scale(x) == 0.25
+    t = torch.from_numpy(x).to(dtype).cuda()
+    _, byte, used = check_quantized(ep, ep.fp4_quantize(t, fmt, **({} if g is None else {"tensor_scale": g})), t, g)
+    assert np.array_equal(R.scale_values(byte, fmt) * used, np.repeat(q[:, None], byte.shape[1], 1))
+    check_borders_met(x, byte, fmt, dtype, used)
+
+
 def test_wait_that_gives_up_is_reported_once(ep):
     """A kernel whose barrier no copy ever reaches gives up after its short limit: the status is raised once,
     and the next product is right."""
