@@ -132,7 +132,9 @@ __device__ __forceinline__ uint2 e4m3_payload(const Raw8<DT>& v, float inv) {
 }
 
 // Scale and reciprocal of an 8-bit row from the bits of its largest element: payload = v * inv, rounded;
-// inv = 0 where the payload is zeros.
+// inv = 0 where the payload is zeros.  int8: s is the product with the float nearest 1/127, as torch divides by a
+// constant on a GPU, so that rows quantised there in elementary operations get the same scale and, with the
+// payload nearest v / s, the same integers.  It is at most a unit in the last place from the rounded amax / 127.
 template <int DT, int FMT>
 __device__ __forceinline__ void row_scale(uint32_t bits, float& s, float& inv) {
     const bool fine = bits < AbsBits<DT>::kInf;

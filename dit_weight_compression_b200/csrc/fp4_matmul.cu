@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_split_kernel(const __grid_con
 // take the sums: they read all of them into registers, give the accumulator back, and write while the next
 // tile's products run.  (Tensor memory: 256 columns of sums leave 256 for scales, so the accumulator is
 // single; handing it back before it is read, which is wrong, would save nothing measurable.)
-// 8192 x 28672 x 8192 nvfp4: 685 us, 5.6 PFLOP/s.  Its copies from L2 bind it (without them 23% less), then
-// the board's power: in loops of a second the clock falls and the same product takes 784 us.
+// 8192 x 28672 x 8192 nvfp4: 677 to 687 us in bursts of three, 5.6 PFLOP/s.  Its copies from L2 bind it (without
+// them 4096 x 9472 x 8192 takes 23% less), then the board's power: in loops of a second the clock falls and
+// the large product takes 790 to 820 us.
 template <bool NV>
 struct PairGeo {
     static constexpr int kScaleTiles = NV ? 4 : 2;

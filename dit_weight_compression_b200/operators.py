@@ -254,7 +254,9 @@ def fp4_matmul(a: FP4Tensor, b: FP4Tensor, *, bias: torch.Tensor | None = None, 
 class KVCache:
     """A paged cache of keys and values, quantised as it is written.  ``k`` and ``v`` hold the payload
     (n_pages x page_size x heads x row: float8_e4m3fn, int8, or packed uint8), ``k_scales`` and
-    ``v_scales`` the scales (float32, one a row; uint8, one a block for the 4-bit formats)."""
+    ``v_scales`` the scales (float32, one a row; uint8, one a block for the 4-bit formats).  It saves
+    memory, not traffic: ``cache_read`` restores dense rows.  ``nvfp4`` rows have no tensor scale: blocks
+    up to 0.0059 become zeros and values above 2688 are clamped; the other formats have no such bounds."""
 
     def __init__(self, n_pages: int, page_size: int, heads: int, head_dim: int, format: str = "fp8", device=None):
         _format(format, CACHE_FORMATS)
@@ -339,8 +341,9 @@ def cache_read(cache: KVCache, page_table: torch.Tensor, cu_seqlens: torch.Tenso
                dtype: torch.dtype = torch.bfloat16, out: tuple | None = None, stream=None) -> tuple:
     """Read sequences back as (k, v), tokens x heads x head_dim.  `page_table` (int32, sequences x pages)
     names the pages of each sequence, `cu_seqlens` (int32, sequences + 1) where each starts among the
-    tokens; `total` is the number of tokens, or `out` the pair of tensors to fill (tokens of it past
-    cu_seqlens[-1] are left as they are).  Positions without a valid page read as zeros."""
+    tokens; `total` is the number of tokens, or `out` the pair of tensors to fill.  Tokens past
+    cu_seqlens[-1] are left as they are: in tensors that the call makes they are not set.  Positions without
+    a valid page read as zeros."""
     for t, what in ((page_table, "page_table"), (cu_seqlens, "cu_seqlens")):
         _cuda(t, what, cache.device)
         if t.dtype != torch.int32:

@@ -288,6 +288,10 @@ int ep_fp4_matmul(const ep_fp4_tensor* a, const ep_fp4_tensor* b, const void* bi
  *                amax < 2^-100; payload the integer nearest v / s (of the exact quotient, ties to
  *                even), 0 where s = 0.
  *   EP_MXFP4, EP_NVFP4   the blocks of the 4-bit formats above along the row, with g = 1.
+ *                EP_NVFP4 rows therefore have the range of E4M3 scales: a block whose largest value is at
+ *                most 6 * 2^-10 (0.0059) is stored as zeros, below 6 * 2^-6 (0.094) its scale has fewer
+ *                than 4 significant bits, and values above 2688 are clamped.  The other formats keep
+ *                rows of any size; values that may be so small or large belong in one of them.
  * A row (4-bit: a block) that holds a NaN or an infinity gets a NaN scale and restores as NaNs. */
 typedef struct {
     void* data;      /* n_pages x page_size x heads x row bytes, 16-byte aligned; row bytes: head_dim for
